@@ -278,7 +278,9 @@ def _plain_combine_grad(state):
 def _plain_codec(state):
     case, x = state["case"], state["x"].float()
     g = x.view(case["rows"], -1, case["group"])
-    scale = (g.abs().amax(2) / 7.0).to(state["x"].dtype)
+    amax = g.abs().amax(2)
+    # divided by a tensor: a number's reciprocal would be multiplied, which rounds twice
+    scale = (amax / torch.full_like(amax, 7.0)).to(state["x"].dtype)
     s = scale.float()[:, :, None]
     q = torch.where(s > 0, torch.round(g / s), 0.0).clamp(-7, 7)
     c = (q + 8).to(torch.uint8).view(case["rows"], -1)
