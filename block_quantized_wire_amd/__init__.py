@@ -1,6 +1,7 @@
 """libblockq: block-quantized wire codecs for AMD MI355X (gfx950).
 
-A thin ctypes binding over the C ABI declared in ``include/blockq.h``.  Every
+A thin ctypes binding over the C ABI declared in ``include/blockq.h`` and
+``include/blockq_moe.h``.  Every
 function here has the name of the C entry point it calls and only marshals
 arguments: torch tensors give device pointers, the stream defaults to torch's
 current stream, and a non-OK status raises :class:`BlockqError`.  All compute
@@ -32,6 +33,12 @@ __all__ = [
     "bq_quant_e4m3_b128", "bq_dequant_e4m3_b128",
     "bq_mx_scale_mfma_bytes", "bq_quant_mx_slice_mfma", "bq_quant_mx_slice_mfma_f16",
     "bq_dequant_mx_mfma", "bq_mm_mx_mfma",
+    "bq_quant_i4", "bq_quant_i4_f16", "bq_dequant_i4", "bq_dequant_i4_f16",
+    "bq_mm_i4", "bq_mm_i4_f16",
+    "bq_moe_sort_ws_bytes", "bq_moe_sort", "bq_moe_gather",
+    "bq_moe_combine", "bq_moe_combine_f16", "bq_moe_combine_f32",
+    "bq_moe_combine_bwd", "bq_moe_combine_bwd_f16", "bq_moe_combine_bwd_f32",
+    "bq_moe_mm_i4", "bq_moe_mm_i4_f16",
     "bq_wire_bytes_b128", "bq_mm_tile_cols", "bq_status_str", "bq_version",
 ]
 
@@ -86,9 +93,23 @@ _SIGS = {
     "bq_quant_mx_slice_mfma_f16": [_P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P],
     "bq_dequant_mx_mfma": [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P],
     "bq_mm_mx_mfma": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P],
+    "bq_quant_i4": [_P, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P],
+    "bq_dequant_i4": [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I, _P, _I64, _P],
+    "bq_mm_i4": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _P, _I64, _P],
+    "bq_moe_sort": [_P, _I64, _I, _I, _P, _P, _P, _P, _I64, _P],
+    "bq_moe_gather": [_P, _I64, _P, _P, _I64, _I, _I, _I64, _I, _P, _I64, _P],
+    "bq_moe_combine": [_P, _I64, _P, _P, _P, _I64, _I, _I, _I64, _P, _I64, _P],
+    "bq_moe_combine_bwd": [_P, _I64, _P, _I64, _P, _P, _P, _I64, _I, _I, _I64, _P, _I64, _P, _P],
+    "bq_moe_mm_i4": [_P, _I64, _I64, _P, _I, _P, _I, _I64, _P, _I64, _I64, _P, _I64, _I64, _P,
+                     _I64, _I64, _I64, _I64, _I, _P, _I64, _P],
     "bq_quant_e4m3_b128": [_P, _I64, _P, _P, _P],
     "bq_dequant_e4m3_b128": [_P, _P, _I64, _P, _P],
 }
+for _name in ("bq_quant_i4", "bq_dequant_i4", "bq_mm_i4", "bq_moe_mm_i4", "bq_moe_combine",
+              "bq_moe_combine_bwd"):
+    _SIGS[_name + "_f16"] = _SIGS[_name]
+for _name in ("bq_moe_combine", "bq_moe_combine_bwd"):
+    _SIGS[_name + "_f32"] = _SIGS[_name]
 _lib = None
 
 
@@ -112,6 +133,8 @@ def _L() -> ctypes.CDLL:
         L.bq_wire_bytes_b128.restype = _I64
         L.bq_mx_scale_mfma_bytes.argtypes = [_I64, _I64]
         L.bq_mx_scale_mfma_bytes.restype = _I64
+        L.bq_moe_sort_ws_bytes.argtypes = [_I64, _I, _I]
+        L.bq_moe_sort_ws_bytes.restype = _I64
         L.bq_mm_tile_cols.argtypes = [_I64, _I64, ctypes.c_int]
         L.bq_mm_tile_cols.restype = ctypes.c_int
         L.bq_status_str.argtypes = [ctypes.c_int]
@@ -462,6 +485,176 @@ def bq_a2a_allreduce_mx(partials, v_send, e_send, red, v_bcast, e_bcast, outs,
            _L().bq_a2a_allreduce_mx(len(partials), n, _ptrs(partials), _ptrs(v_send), _ptrs(e_send),
                                    _ptr(red), _ptr(v_bcast), _ptr(e_bcast), _ptrs(outs),
                                    _stream(stream)))
+
+
+# ---- I4: 4-bit weights with group scales ------------------------------------------------
+#
+# c: torch.uint8 (N, >= K/2), two codes to a byte; scale: (N, >= K/group) in x's type, its row
+# stride a multiple of 4; zero: torch.uint8 like scale, or None (8 everywhere).
+
+def _quant_i4(name, x, c, scale, group, rows, cols, stream):
+    rows = x.shape[0] if rows is None else rows
+    cols = x.shape[1] if cols is None else cols
+    _check(name, getattr(_L(), name)(_ptr(x), rows, cols, x.stride(0), group, _ptr(c), c.stride(0),
+                                     _ptr(scale), scale.stride(0), _stream(stream)))
+
+
+def bq_quant_i4(x, c, scale, group: int = 128, rows: int | None = None, cols: int | None = None,
+                stream=None) -> None:
+    _quant_i4("bq_quant_i4", x, c, scale, group, rows, cols, stream)
+
+
+def bq_quant_i4_f16(x, c, scale, group: int = 128, rows: int | None = None,
+                    cols: int | None = None, stream=None) -> None:
+    """bq_quant_i4 on IEEE binary16 x and scale."""
+    _quant_i4("bq_quant_i4_f16", x, c, scale, group, rows, cols, stream)
+
+
+def _dequant_i4(name, c, scale, y, zero, group, rows, cols, stream):
+    rows = y.shape[0] if rows is None else rows
+    cols = y.shape[1] if cols is None else cols
+    ldz = 0 if zero is None else zero.stride(0)
+    _check(name, getattr(_L(), name)(_ptr(c), c.stride(0), _ptr(scale), scale.stride(0),
+                                     _ptr(zero), ldz, rows, cols, group, _ptr(y), y.stride(0),
+                                     _stream(stream)))
+
+
+def bq_dequant_i4(c, scale, y, zero=None, group: int = 128, rows: int | None = None,
+                  cols: int | None = None, stream=None) -> None:
+    _dequant_i4("bq_dequant_i4", c, scale, y, zero, group, rows, cols, stream)
+
+
+def bq_dequant_i4_f16(c, scale, y, zero=None, group: int = 128, rows: int | None = None,
+                      cols: int | None = None, stream=None) -> None:
+    """bq_dequant_i4 with IEEE binary16 scale and y."""
+    _dequant_i4("bq_dequant_i4_f16", c, scale, y, zero, group, rows, cols, stream)
+
+
+def _mm_i4(name, x, c, scale, y, zero, group, M, N, K, stream):
+    M = x.shape[0] if M is None else M
+    N = y.shape[1] if N is None else N
+    K = x.shape[1] if K is None else K
+    ldz = 0 if zero is None else zero.stride(0)
+    _check(name, getattr(_L(), name)(_ptr(x), x.stride(0), _ptr(c), c.stride(0), _ptr(scale),
+                                     scale.stride(0), _ptr(zero), ldz, M, N, K, group, _ptr(y),
+                                     y.stride(0), _stream(stream)))
+
+
+def bq_mm_i4(x, c, scale, y, zero=None, group: int = 128, M: int | None = None,
+             N: int | None = None, K: int | None = None, stream=None) -> None:
+    """Y = bf16(X W^T): x (M, K) bf16, W the I4 matrix (c, scale, zero) of N rows, y (M, N)."""
+    _mm_i4("bq_mm_i4", x, c, scale, y, zero, group, M, N, K, stream)
+
+
+def bq_mm_i4_f16(x, c, scale, y, zero=None, group: int = 128, M: int | None = None,
+                 N: int | None = None, K: int | None = None, stream=None) -> None:
+    """bq_mm_i4 on IEEE binary16 x, scale and y."""
+    _mm_i4("bq_mm_i4_f16", x, c, scale, y, zero, group, M, N, K, stream)
+
+
+# ---- the expert layer: tokens sorted by expert, expert products, and back ---------------
+#
+# off (experts + 1), src and pos (tokens * topk): torch.int32, as bq_moe_sort writes them;
+# weight and dweight (tokens, topk): torch.float32, contiguous.
+
+def bq_moe_sort_ws_bytes(tokens: int, topk: int, experts: int) -> int:
+    """Scratch bytes of bq_moe_sort (-1 for sizes outside its limits)."""
+    return _L().bq_moe_sort_ws_bytes(tokens, topk, experts)
+
+
+def bq_moe_sort(expert, experts: int, off, src, pos, ws=None, stream=None) -> None:
+    """expert (tokens, topk) torch.int32, contiguous -> off, src, pos; ws: scratch of at least
+    bq_moe_sort_ws_bytes bytes, or None where that is 0."""
+    tokens, topk = expert.shape
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("bq_moe_sort", _L().bq_moe_sort(_ptr(expert), tokens, topk, experts, _ptr(off),
+                                           _ptr(src), _ptr(pos), _ptr(ws), ws_bytes,
+                                           _stream(stream)))
+
+
+def bq_moe_gather(x, pos, off, out, topk: int, cols: int | None = None, stream=None) -> None:
+    """out[pos[t*topk + j]] = x[t]; the rows of dropped slots become 0."""
+    cols = x.shape[1] if cols is None else cols
+    _check("bq_moe_gather",
+           _L().bq_moe_gather(_ptr(x), x.stride(0), _ptr(pos), _ptr(off), x.shape[0], topk,
+                              off.shape[0] - 1, cols, x.element_size(), _ptr(out), out.stride(0),
+                              _stream(stream)))
+
+
+def _moe_combine(name, rows, pos, off, y, weight, topk, cols, stream):
+    cols = y.shape[1] if cols is None else cols
+    _check(name, getattr(_L(), name)(_ptr(rows), rows.stride(0), _ptr(pos), _ptr(off),
+                                     _ptr(weight), y.shape[0], topk, off.shape[0] - 1, cols,
+                                     _ptr(y), y.stride(0), _stream(stream)))
+
+
+def bq_moe_combine(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+                   stream=None) -> None:
+    """y[t] = sum over kept j of weight[t, j] * rows[pos[t*topk + j]] (weight None: 1, which is
+    the gradient of bq_moe_gather)."""
+    _moe_combine("bq_moe_combine", rows, pos, off, y, weight, topk, cols, stream)
+
+
+def bq_moe_combine_f16(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+                       stream=None) -> None:
+    _moe_combine("bq_moe_combine_f16", rows, pos, off, y, weight, topk, cols, stream)
+
+
+def bq_moe_combine_f32(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+                       stream=None) -> None:
+    _moe_combine("bq_moe_combine_f32", rows, pos, off, y, weight, topk, cols, stream)
+
+
+def _moe_combine_bwd(name, dy, rows, pos, off, weight, drows, dweight, cols, stream):
+    cols = dy.shape[1] if cols is None else cols
+    tokens, topk = weight.shape
+    _check(name, getattr(_L(), name)(_ptr(dy), dy.stride(0), _ptr(rows), rows.stride(0), _ptr(pos),
+                                     _ptr(off), _ptr(weight), tokens, topk, off.shape[0] - 1, cols,
+                                     _ptr(drows), drows.stride(0), _ptr(dweight),
+                                     _stream(stream)))
+
+
+def bq_moe_combine_bwd(dy, rows, pos, off, weight, drows, dweight, cols: int | None = None,
+                       stream=None) -> None:
+    """The gradient of bq_moe_combine: drows (sorted rows) and dweight (tokens, topk)."""
+    _moe_combine_bwd("bq_moe_combine_bwd", dy, rows, pos, off, weight, drows, dweight, cols,
+                     stream)
+
+
+def bq_moe_combine_bwd_f16(dy, rows, pos, off, weight, drows, dweight, cols: int | None = None,
+                           stream=None) -> None:
+    _moe_combine_bwd("bq_moe_combine_bwd_f16", dy, rows, pos, off, weight, drows, dweight, cols,
+                     stream)
+
+
+def bq_moe_combine_bwd_f32(dy, rows, pos, off, weight, drows, dweight, cols: int | None = None,
+                           stream=None) -> None:
+    _moe_combine_bwd("bq_moe_combine_bwd_f32", dy, rows, pos, off, weight, drows, dweight, cols,
+                     stream)
+
+
+def _moe_mm_i4(name, x, off, c, scale, y, zero, group, src, topk, N, K, stream):
+    N = y.shape[1] if N is None else N
+    K = x.shape[1] if K is None else K
+    ldz, stride_z = (0, 0) if zero is None else (zero.stride(1), zero.stride(0))
+    _check(name, getattr(_L(), name)(_ptr(x), x.stride(0), x.shape[0], _ptr(src), topk, _ptr(off),
+                                     off.shape[0] - 1, y.shape[0], _ptr(c), c.stride(1),
+                                     c.stride(0), _ptr(scale), scale.stride(1), scale.stride(0),
+                                     _ptr(zero), ldz, stride_z, N, K, group, _ptr(y), y.stride(0),
+                                     _stream(stream)))
+
+
+def bq_moe_mm_i4(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int = 1,
+                 N: int | None = None, K: int | None = None, stream=None) -> None:
+    """y[p] = bf16(X_p W_e^T) for the sorted rows p of every expert e: X_p = x[p], or
+    x[src[p] // topk] where src is given.  c, scale, zero: (experts, N, ...)."""
+    _moe_mm_i4("bq_moe_mm_i4", x, off, c, scale, y, zero, group, src, topk, N, K, stream)
+
+
+def bq_moe_mm_i4_f16(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int = 1,
+                     N: int | None = None, K: int | None = None, stream=None) -> None:
+    """bq_moe_mm_i4 on IEEE binary16 x, scale and y."""
+    _moe_mm_i4("bq_moe_mm_i4_f16", x, off, c, scale, y, zero, group, src, topk, N, K, stream)
 
 
 # ---- E4M3 128-block codec ------------------------------------------------------------------

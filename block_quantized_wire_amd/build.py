@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libblockq.so")
-SOURCES = ["bq_abi.cpp", "bq_i8.hip", "bq_mx.hip", "bq_mxc.hip", "bq_mm.hip", "bq_noalloc.hip"]
+SOURCES = ["bq_abi.cpp", "bq_i8.hip", "bq_mx.hip", "bq_mxc.hip", "bq_mm.hip", "bq_noalloc.hip",
+           "bq_i4.hip", "bq_mmi4.hip", "bq_moe.hip"]
 HEADERS = ["bq_device.h", "bq_launch.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -53,7 +54,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(ROOT, "include", "blockq.h")]
+        os.path.join(ROOT, "include", h) for h in ("blockq.h", "blockq_moe.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -6,6 +6,7 @@
 // Compatibility).  The library allocates nothing, keeps no state and never
 // synchronizes, so every call may be captured in a HIP graph.
 #include "blockq.h"
+#include "blockq_moe.h"
 
 #include <hip/hip_runtime.h>
 
@@ -844,6 +845,451 @@ bq_status bq_mm_mx_mfma(const uint8_t* xv, int64_t ldxv, const uint8_t* xe, int6
     return launched(bq::launch_mm_mx_mfma(xv, ldxv, xe, (xe_rows + 15) / 16, wv, ldwv, we,
                                           (we_rows + 15) / 16, M, N, K, y, ldy,
                                           as_stream(stream)));
+}
+
+// ---- I4: 4-bit weights with group scales ---------------------------------------------------
+
+namespace {
+
+constexpr int64_t kI4MaxDim = (int64_t)1 << 30;    // rows of x, K
+constexpr int64_t kI4MaxN = (int64_t)1 << 26;      // rows of W (a launch holds < 2^32 threads)
+
+bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+// Groups of a row as they are read: whole units of 128 columns.
+int64_t groups_read(int64_t cols, int group) {
+    return (cols + kBlk - 1) / kBlk * (kBlk / group);
+}
+
+// The codes, scales and zero points of `rows` x `cols`.  zero may be null.
+bq_status check_i4(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                   const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols, int group) {
+    if (!c || !scale)
+        return BQ_ERR_NULL;
+    if (ldc < cols / 2 || lds < cols / group || (zero && ldz < cols / group))
+        return BQ_ERR_BOUNDS;
+    if (!extent_fits(rows, cols / 2, ldc, 1) || !extent_fits(rows, cols / group, lds, 2) ||
+        (zero && !extent_fits(rows, cols / group, ldz, 1)))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(c, 16) || ldc % 16 != 0 || !aligned(scale, 8) || lds % 4 != 0 ||
+        (zero && (!aligned(zero, 4) || ldz % 4 != 0)))
+        return BQ_ERR_ALIGN;
+    return BQ_OK;
+}
+
+bool overlaps_i4(Span out, const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                 const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols, int group) {
+    const int64_t groups = groups_read(cols, group);
+    return overlaps(out, span(c, extent(rows, cols / 2, ldc, 1))) ||
+           overlaps(out, span(scale, extent(rows, groups, lds, 2))) ||
+           (zero && overlaps(out, span(zero, extent(rows, groups, ldz, 1))));
+}
+
+// Codec shapes: whole groups, and at most 2^32 units of 8 values.
+bq_status check_i4_shape(int64_t rows, int64_t cols, int group) {
+    if (rows < 0 || cols < 0 || !group_ok(group) || cols % group != 0)
+        return BQ_ERR_SIZE;
+    if (cols > 0 && rows > (((int64_t)1 << 32) - 1) / (cols / 8))
+        return BQ_ERR_SIZE;
+    return BQ_OK;
+}
+
+bq_status quant_i4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int group,
+                   uint8_t* c, int64_t ldc, uint16_t* scale, int64_t lds, bool f16,
+                   void* stream) {
+    BQ_TRY(check_i4_shape(rows, cols, group));
+    if (rows == 0 || cols == 0)
+        return BQ_OK;
+    if (!x)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_i4(c, ldc, scale, lds, nullptr, 0, rows, cols, group));
+    if (ldx < cols || !extent_fits(rows, cols, ldx, 2))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(x, 16) || ldx % 8 != 0)
+        return BQ_ERR_ALIGN;
+    const Span xs = span(x, extent(rows, cols, ldx, 2));
+    const Span cs = span(c, extent(rows, cols / 2, ldc, 1));
+    const Span ss = span(scale, extent(rows, cols / group, lds, 2));
+    if (overlaps(xs, cs) || overlaps(xs, ss) || overlaps(cs, ss))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_quant_i4(x, rows, cols, ldx, group, c, ldc, scale, lds, f16,
+                                        as_stream(stream)));
+}
+
+bq_status dequant_i4(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                     const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols, int group,
+                     uint16_t* y, int64_t ldy, bool f16, void* stream) {
+    BQ_TRY(check_i4_shape(rows, cols, group));
+    if (rows == 0 || cols == 0)
+        return BQ_OK;
+    if (!y)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_i4(c, ldc, scale, lds, zero, ldz, rows, cols, group));
+    if (ldy < cols || !extent_fits(rows, cols, ldy, 2))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(y, 16) || ldy % 8 != 0)
+        return BQ_ERR_ALIGN;
+    if (overlaps_i4(span(y, extent(rows, cols, ldy, 2)), c, ldc, scale, lds, zero, ldz, rows, cols,
+                    group))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_dequant_i4(c, ldc, scale, lds, zero, ldz, rows, cols, group, y, ldy,
+                                          f16, as_stream(stream)));
+}
+
+// The shared checks of the products: x of x_rows rows, y of `rows` rows, W of N x K.
+bq_status check_i4_mm(const bq::I4Mm& m, int64_t x_rows, int64_t rows, int64_t N, int64_t K,
+                      int group) {
+    if (!m.x || !m.y)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_i4(m.c, m.ldc, m.s, m.lds, m.z, m.ldz, N, K, group));
+    if (m.ldx < K || m.ldy < N || !extent_fits(x_rows, K, m.ldx, 2) ||
+        !extent_fits(rows, N, m.ldy, 2))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(m.x, 16) || m.ldx % 8 != 0 || !aligned(m.y, 2))
+        return BQ_ERR_ALIGN;
+    return BQ_OK;
+}
+
+bq_status mm_i4(const uint16_t* x, int64_t ldx, const uint8_t* c, int64_t ldc,
+                const uint16_t* scale, int64_t lds, const uint8_t* zero, int64_t ldz, int64_t M,
+                int64_t N, int64_t K, int group, uint16_t* y, int64_t ldy, bool f16,
+                void* stream) {
+    if (M < 0 || N < 0 || K <= 0 || !group_ok(group) || K % group != 0 || M > kI4MaxDim ||
+        N > kI4MaxN || K > kI4MaxDim)
+        return BQ_ERR_SIZE;
+    if (M == 0 || N == 0)
+        return BQ_OK;
+    bq::I4Mm m{};
+    m.x = x;
+    m.c = c;
+    m.s = scale;
+    m.z = zero;
+    m.y = y;
+    m.ldx = ldx;
+    m.ldc = ldc;
+    m.lds = lds;
+    m.ldz = ldz;
+    m.ldy = ldy;
+    m.rows = m.x_rows = (int32_t)M;
+    m.N = (int32_t)N;
+    m.K = (int32_t)K;
+    m.topk = 1;
+    m.experts = 1;
+    BQ_TRY(check_i4_mm(m, M, M, N, K, group));
+    const Span ys = span(y, extent(M, N, ldy, 2));
+    if (overlaps(ys, span(x, extent(M, K, ldx, 2))) ||
+        overlaps_i4(ys, c, ldc, scale, lds, zero, ldz, N, K, group))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_mm_i4(m, group, f16, as_stream(stream)));
+}
+
+}  // namespace
+
+bq_status bq_quant_i4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int group,
+                      uint8_t* c, int64_t ldc, uint16_t* scale, int64_t lds, void* stream) {
+    return quant_i4(x, rows, cols, ldx, group, c, ldc, scale, lds, false, stream);
+}
+
+bq_status bq_quant_i4_f16(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int group,
+                          uint8_t* c, int64_t ldc, uint16_t* scale, int64_t lds, void* stream) {
+    return quant_i4(x, rows, cols, ldx, group, c, ldc, scale, lds, true, stream);
+}
+
+bq_status bq_dequant_i4(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                        const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols, int group,
+                        uint16_t* y, int64_t ldy, void* stream) {
+    return dequant_i4(c, ldc, scale, lds, zero, ldz, rows, cols, group, y, ldy, false, stream);
+}
+
+bq_status bq_dequant_i4_f16(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                            const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols,
+                            int group, uint16_t* y, int64_t ldy, void* stream) {
+    return dequant_i4(c, ldc, scale, lds, zero, ldz, rows, cols, group, y, ldy, true, stream);
+}
+
+bq_status bq_mm_i4(const uint16_t* x, int64_t ldx, const uint8_t* c, int64_t ldc,
+                   const uint16_t* scale, int64_t lds, const uint8_t* zero, int64_t ldz,
+                   int64_t M, int64_t N, int64_t K, int group, uint16_t* y, int64_t ldy,
+                   void* stream) {
+    return mm_i4(x, ldx, c, ldc, scale, lds, zero, ldz, M, N, K, group, y, ldy, false, stream);
+}
+
+bq_status bq_mm_i4_f16(const uint16_t* x, int64_t ldx, const uint8_t* c, int64_t ldc,
+                       const uint16_t* scale, int64_t lds, const uint8_t* zero, int64_t ldz,
+                       int64_t M, int64_t N, int64_t K, int group, uint16_t* y, int64_t ldy,
+                       void* stream) {
+    return mm_i4(x, ldx, c, ldc, scale, lds, zero, ldz, M, N, K, group, y, ldy, true, stream);
+}
+
+// ---- the expert layer ----------------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;
+
+bq_status check_moe(int64_t tokens, int topk, int experts) {
+    if (topk < 1 || topk > BQ_MAX_TOPK || experts < 1 || experts > BQ_MAX_EXPERTS)
+        return BQ_ERR_NSRC;
+    if (tokens < 0 || tokens > (kMaxSlots - 1) / topk)
+        return BQ_ERR_SIZE;
+    return BQ_OK;
+}
+
+// pos and off, which every call on rows reads, and the column count.
+bq_status check_moe_rows(const bq::MoeRows& r) {
+    if (r.cols < 0 || r.cols > kI4MaxDim)
+        return BQ_ERR_SIZE;
+    return BQ_OK;
+}
+
+bq_status check_order(const bq::MoeRows& r) {
+    if (!r.pos || !r.off)
+        return BQ_ERR_NULL;
+    return aligned(r.pos, 4) && aligned(r.off, 4) ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+bool overlaps_order(Span out, const bq::MoeRows& r) {
+    return overlaps(out, span(r.pos, 4 * r.tokens * r.topk)) ||
+           overlaps(out, span(r.off, 4 * ((int64_t)r.experts + 1)));
+}
+
+bq_status moe_combine(const void* rows, int64_t ldr, const int32_t* pos, const int32_t* off,
+                      const float* weight, int64_t tokens, int topk, int experts, int64_t cols,
+                      void* y, int64_t ldy, bq::MoeType type, void* stream) {
+    const int64_t es = type == bq::MoeType::kF32 ? 4 : 2;
+    const bq::MoeRows r{pos, off, tokens, topk, experts, cols};
+    BQ_TRY(check_moe(tokens, topk, experts));
+    BQ_TRY(check_moe_rows(r));
+    if (tokens == 0 || cols == 0)
+        return BQ_OK;
+    if (!rows || !y)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_order(r));
+    const int64_t slots = tokens * topk;
+    if (ldr < cols || ldy < cols || !extent_fits(slots, cols, ldr, es) ||
+        !extent_fits(tokens, cols, ldy, es))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(rows, es) || !aligned(y, es) || !aligned(weight, 4))
+        return BQ_ERR_ALIGN;
+    const Span ys = span(y, extent(tokens, cols, ldy, es));
+    if (overlaps(ys, span(rows, extent(slots, cols, ldr, es))) || overlaps_order(ys, r) ||
+        (weight && overlaps(ys, span(weight, 4 * slots))))
+        return BQ_ERR_ALIAS;
+    return launched(
+        bq::launch_moe_combine(r, type, rows, ldr, weight, y, ldy, as_stream(stream)));
+}
+
+bq_status moe_combine_bwd(const void* dy, int64_t lddy, const void* rows, int64_t ldr,
+                          const int32_t* pos, const int32_t* off, const float* weight,
+                          int64_t tokens, int topk, int experts, int64_t cols, void* drows,
+                          int64_t lddr, float* dweight, bq::MoeType type, void* stream) {
+    const int64_t es = type == bq::MoeType::kF32 ? 4 : 2;
+    const bq::MoeRows r{pos, off, tokens, topk, experts, cols};
+    BQ_TRY(check_moe(tokens, topk, experts));
+    BQ_TRY(check_moe_rows(r));
+    if (tokens == 0)
+        return BQ_OK;
+    if (!dy || !rows || !weight || !drows || !dweight)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_order(r));
+    const int64_t slots = tokens * topk;
+    if (lddy < cols || ldr < cols || lddr < cols || !extent_fits(tokens, cols, lddy, es) ||
+        !extent_fits(slots, cols, ldr, es) || !extent_fits(slots, cols, lddr, es))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(dy, es) || !aligned(rows, es) || !aligned(drows, es) || !aligned(weight, 4) ||
+        !aligned(dweight, 4))
+        return BQ_ERR_ALIGN;
+    const Span outs[2] = {span(drows, extent(slots, cols, lddr, es)), span(dweight, 4 * slots)};
+    const Span ins[3] = {span(dy, extent(tokens, cols, lddy, es)),
+                         span(rows, extent(slots, cols, ldr, es)), span(weight, 4 * slots)};
+    if (any_overlap(outs, 2, ins, 3) || overlaps_order(outs[0], r) || overlaps_order(outs[1], r))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_moe_combine_bwd(r, type, dy, lddy, rows, ldr, weight, drows, lddr,
+                                               dweight, as_stream(stream)));
+}
+
+bq_status moe_mm_i4(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* src, int topk,
+                    const int32_t* off, int experts, int64_t rows, const uint8_t* c, int64_t ldc,
+                    int64_t stride_c, const uint16_t* scale, int64_t lds, int64_t stride_s,
+                    const uint8_t* zero, int64_t ldz, int64_t stride_z, int64_t N, int64_t K,
+                    int group, uint16_t* y, int64_t ldy, bool f16, void* stream) {
+    if (experts < 1 || experts > BQ_MAX_EXPERTS || (src && (topk < 1 || topk > BQ_MAX_TOPK)))
+        return BQ_ERR_NSRC;
+    if (rows < 0 || x_rows < 0 || N < 0 || K <= 0 || !group_ok(group) || K % group != 0 ||
+        rows >= kMaxSlots || x_rows > kI4MaxDim || N > kI4MaxN || K > kI4MaxDim)
+        return BQ_ERR_SIZE;
+    if (!src && x_rows < rows)
+        return BQ_ERR_BOUNDS;
+    if (rows == 0 || N == 0)
+        return BQ_OK;
+    bq::I4Mm m{};
+    m.x = x;
+    m.src = src;
+    m.off = off;
+    m.c = c;
+    m.s = scale;
+    m.z = zero;
+    m.y = y;
+    m.ldx = ldx;
+    m.ldc = ldc;
+    m.lds = lds;
+    m.ldz = ldz;
+    m.ldy = ldy;
+    m.stride_c = stride_c;
+    m.stride_s = stride_s;
+    m.stride_z = stride_z;
+    m.rows = (int32_t)rows;
+    m.x_rows = (int32_t)x_rows;
+    m.N = (int32_t)N;
+    m.K = (int32_t)K;
+    m.topk = src ? topk : 1;
+    m.experts = experts;
+    if (!off)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_i4_mm(m, x_rows, rows, N, K, group));
+    if (experts > 1) {
+        // whole matrices lie apart, and all of them within the largest operand
+        if (stride_c < extent(N, K / 2, ldc, 1) || stride_s < extent(N, K / group, lds, 1) ||
+            (zero && stride_z < extent(N, K / group, ldz, 1)))
+            return BQ_ERR_BOUNDS;
+        const int64_t lim = kMaxExtentBytes / experts / 2;
+        if (stride_c > lim || stride_s > lim || (zero && stride_z > lim))
+            return BQ_ERR_BOUNDS;
+        if (stride_c % 16 != 0 || stride_s % 4 != 0 || (zero && stride_z % 4 != 0))
+            return BQ_ERR_ALIGN;
+    }
+    if (!aligned(off, 4) || (src && !aligned(src, 4)))
+        return BQ_ERR_ALIGN;
+    const Span ys = span(y, extent(rows, N, ldy, 2));
+    const int64_t last = experts - 1, groups = groups_read(K, group);
+    if (overlaps(ys, span(x, extent(x_rows, K, ldx, 2))) ||
+        overlaps(ys, span(off, 4 * ((int64_t)experts + 1))) ||
+        (src && overlaps(ys, span(src, 4 * rows))) ||
+        overlaps(ys, span(c, last * stride_c + extent(N, K / 2, ldc, 1))) ||
+        overlaps(ys, span(scale, 2 * last * stride_s + extent(N, groups, lds, 2))) ||
+        (zero && overlaps(ys, span(zero, last * stride_z + extent(N, groups, ldz, 1)))))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_mm_i4(m, group, f16, as_stream(stream)));
+}
+
+}  // namespace
+
+int64_t bq_moe_sort_ws_bytes(int64_t tokens, int topk, int experts) {
+    if (check_moe(tokens, topk, experts) != BQ_OK)
+        return -1;
+    if (tokens * topk <= bq::kMoeSortOneBlock)
+        return 0;
+    return 4 * bq::kMoeSortBlocks * ((int64_t)experts + 1);
+}
+
+bq_status bq_moe_sort(const int32_t* expert, int64_t tokens, int topk, int experts, int32_t* off,
+                      int32_t* src, int32_t* pos, void* ws, int64_t ws_bytes, void* stream) {
+    BQ_TRY(check_moe(tokens, topk, experts));
+    const int64_t slots = tokens * topk, need = bq_moe_sort_ws_bytes(tokens, topk, experts);
+    if (!off || (slots > 0 && (!expert || !src || !pos)))
+        return BQ_ERR_NULL;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return BQ_ERR_SCRATCH;
+    if (!aligned(expert, 4) || !aligned(off, 4) || !aligned(src, 4) || !aligned(pos, 4) ||
+        (need > 0 && !aligned(ws, 4)))
+        return BQ_ERR_ALIGN;
+    const Span outs[4] = {span(off, 4 * ((int64_t)experts + 1)), span(src, 4 * slots),
+                          span(pos, 4 * slots), span(ws, need)};
+    const Span in = span(expert, 4 * slots);
+    if (any_overlap(outs, 4, &in, 1))
+        return BQ_ERR_ALIAS;
+    return launched(
+        bq::launch_moe_sort(expert, slots, experts, off, src, pos, ws, as_stream(stream)));
+}
+
+bq_status bq_moe_gather(const void* x, int64_t ldx, const int32_t* pos, const int32_t* off,
+                        int64_t tokens, int topk, int experts, int64_t cols, int esize, void* out,
+                        int64_t ldo, void* stream) {
+    const bq::MoeRows r{pos, off, tokens, topk, experts, cols};
+    BQ_TRY(check_moe(tokens, topk, experts));
+    BQ_TRY(check_moe_rows(r));
+    if (esize != 2 && esize != 4)
+        return BQ_ERR_SIZE;
+    if (tokens == 0 || cols == 0)
+        return BQ_OK;
+    if (!x || !out)
+        return BQ_ERR_NULL;
+    BQ_TRY(check_order(r));
+    const int64_t slots = tokens * topk;
+    if (ldx < cols || ldo < cols || !extent_fits(tokens, cols, ldx, esize) ||
+        !extent_fits(slots, cols, ldo, esize))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(x, esize) || !aligned(out, esize))
+        return BQ_ERR_ALIGN;
+    const Span os = span(out, extent(slots, cols, ldo, esize));
+    if (overlaps(os, span(x, extent(tokens, cols, ldx, esize))) || overlaps_order(os, r))
+        return BQ_ERR_ALIAS;
+    return launched(bq::launch_moe_gather(r, x, ldx, esize, out, ldo, as_stream(stream)));
+}
+
+bq_status bq_moe_combine(const uint16_t* rows, int64_t ldr, const int32_t* pos, const int32_t* off,
+                         const float* weight, int64_t tokens, int topk, int experts, int64_t cols,
+                         uint16_t* y, int64_t ldy, void* stream) {
+    return moe_combine(rows, ldr, pos, off, weight, tokens, topk, experts, cols, y, ldy,
+                       bq::MoeType::kBf16, stream);
+}
+
+bq_status bq_moe_combine_f16(const uint16_t* rows, int64_t ldr, const int32_t* pos,
+                             const int32_t* off, const float* weight, int64_t tokens, int topk,
+                             int experts, int64_t cols, uint16_t* y, int64_t ldy, void* stream) {
+    return moe_combine(rows, ldr, pos, off, weight, tokens, topk, experts, cols, y, ldy,
+                       bq::MoeType::kF16, stream);
+}
+
+bq_status bq_moe_combine_f32(const float* rows, int64_t ldr, const int32_t* pos,
+                             const int32_t* off, const float* weight, int64_t tokens, int topk,
+                             int experts, int64_t cols, float* y, int64_t ldy, void* stream) {
+    return moe_combine(rows, ldr, pos, off, weight, tokens, topk, experts, cols, y, ldy,
+                       bq::MoeType::kF32, stream);
+}
+
+bq_status bq_moe_combine_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* rows, int64_t ldr,
+                             const int32_t* pos, const int32_t* off, const float* weight,
+                             int64_t tokens, int topk, int experts, int64_t cols, uint16_t* drows,
+                             int64_t lddr, float* dweight, void* stream) {
+    return moe_combine_bwd(dy, lddy, rows, ldr, pos, off, weight, tokens, topk, experts, cols,
+                           drows, lddr, dweight, bq::MoeType::kBf16, stream);
+}
+
+bq_status bq_moe_combine_bwd_f16(const uint16_t* dy, int64_t lddy, const uint16_t* rows,
+                                 int64_t ldr, const int32_t* pos, const int32_t* off,
+                                 const float* weight, int64_t tokens, int topk, int experts,
+                                 int64_t cols, uint16_t* drows, int64_t lddr, float* dweight,
+                                 void* stream) {
+    return moe_combine_bwd(dy, lddy, rows, ldr, pos, off, weight, tokens, topk, experts, cols,
+                           drows, lddr, dweight, bq::MoeType::kF16, stream);
+}
+
+bq_status bq_moe_combine_bwd_f32(const float* dy, int64_t lddy, const float* rows, int64_t ldr,
+                                 const int32_t* pos, const int32_t* off, const float* weight,
+                                 int64_t tokens, int topk, int experts, int64_t cols, float* drows,
+                                 int64_t lddr, float* dweight, void* stream) {
+    return moe_combine_bwd(dy, lddy, rows, ldr, pos, off, weight, tokens, topk, experts, cols,
+                           drows, lddr, dweight, bq::MoeType::kF32, stream);
+}
+
+bq_status bq_moe_mm_i4(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* src, int topk,
+                       const int32_t* off, int experts, int64_t rows, const uint8_t* c,
+                       int64_t ldc, int64_t stride_c, const uint16_t* scale, int64_t lds,
+                       int64_t stride_s, const uint8_t* zero, int64_t ldz, int64_t stride_z,
+                       int64_t N, int64_t K, int group, uint16_t* y, int64_t ldy, void* stream) {
+    return moe_mm_i4(x, ldx, x_rows, src, topk, off, experts, rows, c, ldc, stride_c, scale, lds,
+                     stride_s, zero, ldz, stride_z, N, K, group, y, ldy, false, stream);
+}
+
+bq_status bq_moe_mm_i4_f16(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* src,
+                           int topk, const int32_t* off, int experts, int64_t rows,
+                           const uint8_t* c, int64_t ldc, int64_t stride_c, const uint16_t* scale,
+                           int64_t lds, int64_t stride_s, const uint8_t* zero, int64_t ldz,
+                           int64_t stride_z, int64_t N, int64_t K, int group, uint16_t* y,
+                           int64_t ldy, void* stream) {
+    return moe_mm_i4(x, ldx, x_rows, src, topk, off, experts, rows, c, ldc, stride_c, scale, lds,
+                     stride_s, zero, ldz, stride_z, N, K, group, y, ldy, true, stream);
 }
 
 // ---- E4M3 128-block codec ------------------------------------------------------------------

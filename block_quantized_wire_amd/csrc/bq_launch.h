@@ -96,4 +96,55 @@ hipError_t launch_quant_e4m3_b128(const uint16_t* x, uint8_t* v, float* s, int64
 hipError_t launch_dequant_e4m3_b128(const uint8_t* v, const float* s, uint16_t* y, int64_t n,
                                     hipStream_t stream);
 
+// The I4 codec.  f16: x, scale and y hold IEEE binary16 values instead of bf16.
+// rows * (cols / 8) < 2^32.
+hipError_t launch_quant_i4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int group,
+                           uint8_t* c, int64_t ldc, uint16_t* scale, int64_t lds, bool f16,
+                           hipStream_t stream);
+hipError_t launch_dequant_i4(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
+                             const uint8_t* zero, int64_t ldz, int64_t rows, int64_t cols,
+                             int group, uint16_t* y, int64_t ldy, bool f16, hipStream_t stream);
+
+// Products with I4 weights: y = x W^T.  Dense: off is null, `rows` rows of x and y.  Experts:
+// row p in [off[e], off[e+1]) of y is x's row p, or src[p] / topk where src is not null.
+struct I4Mm {
+    const uint16_t* x;
+    const int32_t* src;
+    const int32_t* off;
+    const uint8_t* c;
+    const uint16_t* s;
+    const uint8_t* z;
+    uint16_t* y;
+    int64_t ldx, ldc, lds, ldz, ldy;
+    int64_t stride_c, stride_s, stride_z;
+    int32_t rows, x_rows, N, K;
+    int32_t topk, experts;
+};
+hipError_t launch_mm_i4(const I4Mm& a, int group, bool f16, hipStream_t stream);
+
+// Tokens sorted by expert.  Sorts of up to kMoeSortOneBlock slots take one workgroup and no
+// scratch, larger ones at most kMoeSortBlocks workgroups and one count per bucket and
+// workgroup.
+constexpr int64_t kMoeSortOneBlock = 8192;
+constexpr int64_t kMoeSortBlocks = 256;
+hipError_t launch_moe_sort(const int32_t* expert, int64_t slots, int experts, int32_t* off,
+                           int32_t* src, int32_t* pos, void* ws, hipStream_t stream);
+
+// Rows out and back: the order and the shape every call shares.
+struct MoeRows {
+    const int32_t* pos;
+    const int32_t* off;
+    int64_t tokens;
+    int topk, experts;
+    int64_t cols;
+};
+enum class MoeType { kBf16, kF16, kF32 };
+hipError_t launch_moe_gather(const MoeRows& r, const void* x, int64_t ldx, int esize, void* out,
+                             int64_t ldo, hipStream_t stream);
+hipError_t launch_moe_combine(const MoeRows& r, MoeType type, const void* rows, int64_t ldr,
+                              const float* weight, void* y, int64_t ldy, hipStream_t stream);
+hipError_t launch_moe_combine_bwd(const MoeRows& r, MoeType type, const void* dy, int64_t lddy,
+                                  const void* rows, int64_t ldr, const float* weight, void* drows,
+                                  int64_t lddr, float* dweight, hipStream_t stream);
+
 }  // namespace bq
