@@ -856,10 +856,8 @@ constexpr int64_t kI4MaxN = (int64_t)1 << 26;      // rows of W (a launch holds 
 
 bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 
-// Groups of a row as they are read: whole units of 128 columns.
-int64_t groups_read(int64_t cols, int group) {
-    return (cols + kBlk - 1) / kBlk * (kBlk / group);
-}
+// Entries of a row of scales or zero points as they are read: whole fours.
+int64_t groups_read(int64_t cols, int group) { return (cols / group + 3) / 4 * 4; }
 
 // The codes, scales and zero points of `rows` x `cols`.  zero may be null.
 bq_status check_i4(const uint8_t* c, int64_t ldc, const uint16_t* scale, int64_t lds,
@@ -1118,10 +1116,10 @@ bq_status moe_mm_i4(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_
     if (rows < 0 || x_rows < 0 || N < 0 || K <= 0 || !group_ok(group) || K % group != 0 ||
         rows >= kMaxSlots || x_rows > kI4MaxDim || N > kI4MaxN || K > kI4MaxDim)
         return BQ_ERR_SIZE;
-    if (!src && x_rows < rows)
-        return BQ_ERR_BOUNDS;
     if (rows == 0 || N == 0)
         return BQ_OK;
+    if (x_rows < (src ? 1 : rows))
+        return BQ_ERR_BOUNDS;
     bq::I4Mm m{};
     m.x = x;
     m.src = src;

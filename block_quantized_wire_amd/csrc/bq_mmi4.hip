@@ -19,8 +19,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTK = 128;         // columns of a step: 16 bytes of codes per lane
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kUnit = 256;       // columns of a unit: 128 bytes of codes of a row
 
 template <bool F16>
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
@@ -50,20 +49,28 @@ __device__ __forceinline__ uint16_t from_f32(float f) {
 
 // The 8 codes of a word as operands 16 + code, in the order 0,4, 1,5, 2,6, 3,7 (codes i and
 // i+4 are 16 bits apart).  The code's bits go to the top of the significand: bits 3..6 of
-// a bf16 16.0 (0x4180), bits 6..9 of a binary16 16.0 (0x4C00).
+// a bf16 16.0 (0x4180), bits 6..9 of a binary16 16.0 (0x4C00).  The mask and the base are held
+// in registers, so that the two steps are one shift and one and-or (an instruction takes no
+// two literals).
 template <bool F16>
-__device__ __forceinline__ u32x4 operands(uint32_t w) {
-    constexpr uint32_t mask = F16 ? 0x03C003C0u : 0x00780078u;
-    constexpr uint32_t base = F16 ? 0x4C004C00u : 0x41804180u;
-    constexpr int up = F16 ? 6 : 3;
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = 4 * i < up ? w << (up - 4 * i) : w >> (4 * i - up);
-        r[i] = (v & mask) | base;
+struct Codes {
+    uint32_t mask, base;
+    __device__ __forceinline__ Codes()
+        : mask(F16 ? 0x03C003C0u : 0x00780078u), base(F16 ? 0x4C004C00u : 0x41804180u) {
+        asm("" : "+s"(mask));
+        asm("" : "+v"(base));
     }
-    return r;
-}
+    __device__ __forceinline__ u32x4 operands(uint32_t w) const {
+        constexpr int up = F16 ? 6 : 3;
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = 4 * i < up ? w << (up - 4 * i) : w >> (4 * i - up);
+            r[i] = (v & mask) | base;
+        }
+        return r;
+    }
+};
 
 // 8 values of x (16 bytes) in the operands' order.
 __device__ __forceinline__ u32x4 in_order(u32x4 x) {
@@ -73,88 +80,99 @@ __device__ __forceinline__ u32x4 in_order(u32x4 x) {
                  __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
 }
 
-// A lane loads 32 consecutive columns of its row: lane quarter g has columns [32g, 32g+32) of
-// the 128.  Word j of every quarter is one matrix instruction's 32 columns, which belong to
-// one group only where G is 128.  For smaller groups the words trade places between the
-// quarters: exchanging the halves of the wave puts the columns of each 64 together, and
-// exchanging odd and even quarters then those of each 32.
-template <int G>
-__device__ __forceinline__ void regroup(u32x4& q) {
-    if constexpr (G <= 64) {
-        auto a = __builtin_amdgcn_permlane32_swap(q.x, q.z, false, false);
-        auto b = __builtin_amdgcn_permlane32_swap(q.y, q.w, false, false);
-        q = u32x4{a[0], b[0], a[1], b[1]};
-    }
-    if constexpr (G == 32) {
-        auto a = __builtin_amdgcn_permlane16_swap(q.x, q.y, false, false);
-        auto b = __builtin_amdgcn_permlane16_swap(q.z, q.w, false, false);
-        q = u32x4{a[0], a[1], b[0], b[1]};
-    }
-}
-
-// The first of the 8 columns that lane quarter g feeds into matrix instruction j of a step.
-template <int G>
-__device__ __forceinline__ int col_of(int j, int g) {
-    if constexpr (G == 128)
-        return 32 * g + 8 * j;
-    else if constexpr (G == 64)
-        return 64 * (j >> 1) + 32 * (g & 1) + 16 * (g >> 1) + 8 * (j & 1);
-    else
-        return 32 * j + 8 * g;
+// A lane loads 32 consecutive columns of its row of W: lane quarter g has columns [32g, 32g+32)
+// of 128, 8 to a word.  The four words of the four quarters are exchanged (halves of the wave
+// first, then odd and even quarters), so that word j holds columns [32j + 8g, 32j + 8g + 8):
+// one matrix instruction then takes 32 adjacent columns, which lie in one group, and its
+// operand of x is 64 adjacent bytes of each row.
+__device__ __forceinline__ u32x4 exchange(u32x4 q) {
+    const auto a = __builtin_amdgcn_permlane32_swap(q.x, q.z, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(q.y, q.w, false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{c[0], c[1], d[0], d[1]};
 }
 
 struct Args : I4Mm {
-    int32_t steps;      // ceil(K / 128)
+    int32_t units;      // ceil(K / 256)
     int32_t chunk;      // row chunks between two of a workgroup's (dense)
+    int32_t block0;     // first row block of a launch of many
 };
 
-// One step's data of one block of 16 rows of W: the lane's codes, and the scales and zero
-// points of its row's 128 / G groups.
+// The row of x that row m of y is made from, and whether a source names one that is there (a
+// row whose source is out of range gives zeros, and reads row 0 meanwhile).
+__device__ __forceinline__ bool x_row_ok(const Args& p, int m) {
+    return !p.src || (uint32_t)(p.src[m] / p.topk) < (uint32_t)p.x_rows;
+}
+__device__ __forceinline__ int64_t x_row(const Args& p, int m) {
+    if (!p.src)
+        return m;
+    const int r = p.src[m] / p.topk;
+    return (uint32_t)r < (uint32_t)p.x_rows ? r : 0;
+}
+
+// One unit's data of one block of 16 rows of W: 256 columns are one 128-byte line of codes of
+// each row, and the scales and zero points of a row's 256 / G groups.
 template <int G, bool Z>
-struct Step {
-    static constexpr int kGroups = kTK / G;
-    u32x4 q;
-    uint32_t s[kGroups];
-    uint32_t z;
+struct Weights {
+    u32x4 q[2];
+    uint32_t s[kUnit / G / 2];            // two scales to a word
+    uint32_t z[G == 32 ? 2 : 1];          // four zero points to a word
 };
 
-template <int G, bool Z>
-__device__ __forceinline__ void load_step(Step<G, Z>& st, const uint8_t* c, const uint16_t* s,
-                                          const uint8_t* z, int step, int g, int K) {
-    constexpr int kGroups = kTK / G;
-    const int k = step * kTK + 32 * g;
-    st.q = k < K ? ld16(c + k / 2) : u32x4{};
-    if constexpr (kGroups == 1) {
-        st.s[0] = s[step];
-    } else if constexpr (kGroups == 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(s + step * 2);
-        st.s[0] = v & 0xFFFFu;
-        st.s[1] = v >> 16;
-    } else {
-        const u32x2 v = ld8(s + step * 4);
-        st.s[0] = v.x & 0xFFFFu;
-        st.s[1] = v.x >> 16;
-        st.s[2] = v.y & 0xFFFFu;
-        st.s[3] = v.y >> 16;
+template <int G, bool Z, bool Tail>
+__device__ __forceinline__ void load_unit(Weights<G, Z>& w, const uint8_t* c, const uint16_t* s,
+                                          const uint8_t* z, int unit, int g, int K) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int k = unit * kUnit + h * 128 + 32 * g;
+        w.q[h] = ld16(c + (Tail ? min(k, K - 32) : k) / 2);
     }
-    if constexpr (Z) {
-        if constexpr (kGroups == 1)
-            st.z = z[step];
-        else if constexpr (kGroups == 2)
-            st.z = *reinterpret_cast<const uint16_t*>(z + step * 2);
-        else
-            st.z = *reinterpret_cast<const uint32_t*>(z + step * 4);
+    if constexpr (G == 128) {
+        w.s[0] = *reinterpret_cast<const uint32_t*>(s + unit * 2);
+        if constexpr (Z)
+            w.z[0] = *reinterpret_cast<const uint16_t*>(z + unit * 2);
+    } else if constexpr (G == 64) {
+        const u32x2 v = ld8(s + unit * 4);
+        w.s[0] = v.x;
+        w.s[1] = v.y;
+        if constexpr (Z)
+            w.z[0] = *reinterpret_cast<const uint32_t*>(z + unit * 4);
+    } else {
+        // rows of scales are whole fours of groups, which a unit may have one or two of
+        const int second = Tail ? min(unit * 8 + 4, (K / 32 - 1) & ~3) : unit * 8 + 4;
+        const u32x2 u = ld8(s + unit * 8), v = ld8(s + second);
+        w.s[0] = u.x;
+        w.s[1] = u.y;
+        w.s[2] = v.x;
+        w.s[3] = v.y;
+        if constexpr (Z) {
+            w.z[0] = *reinterpret_cast<const uint32_t*>(z + unit * 8);
+            w.z[1] = *reinterpret_cast<const uint32_t*>(z + second);
+        }
     }
 }
 
+// Everything a wave reads for a unit: R blocks of 16 weight rows, and the 8 operands of x of
+// MT blocks of 16 tokens.
+template <int G, bool Z, int MT, int R>
+struct Buf {
+    Weights<G, Z> w[R];
+    u32x4 x[MT][8];
+};
+
+// Few rows of x: the bytes of the weights bound this kernel, so it streams them once, straight
+// into registers, D units of 256 columns ahead.  A workgroup takes R blocks of 16 weight rows
+// and KW waves that take the units in turn; their sums meet in LDS in wave order.
 // NI results per lane and block of 16 tokens: the token of lane quarter g's result i is
-// g + 4i, so a block of 4 tokens needs one result per lane.  MT blocks of tokens, R blocks of
-// 16 weight rows per workgroup.  The 8 waves share the steps, and their sums meet in LDS.
-template <bool F16, int G, bool Z, int NI, int MT, int R>
-__global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
-    constexpr int kGroups = kTK / G, kPer = 4 / kGroups;
-    constexpr int kTokens = MT == 1 ? 4 * NI : 16 * MT;
-    __shared__ float red[kWaves][R * MT * NI][64];
+// g + 4i, so up to 4 tokens need one result per lane, up to 8 two.  MT > 1 only with NI = 4.
+// Tail: K is not a multiple of 256.  The columns that the last unit lacks are whole groups:
+// their loads are moved to columns that are there, and the groups are left out.
+template <bool F16, int G, bool Z, bool Tail, int NI, int MT, int R, int KW, int D>
+__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) void k_mv_i4(Args p) {
+    constexpr int kGroups = kUnit / G, kPer = 8 / kGroups;
+    constexpr int kTokens = 16 * (MT - 1) + 4 * NI;
+    __shared__ float red[KW][R * MT * NI][64];
     const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * R;
@@ -171,6 +189,8 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
         s += e * p.stride_s;
         z += e * p.stride_z;
     }
+    if (lo >= hi)
+        return;
     const uint8_t* cr[R];
     const uint16_t* sr[R];
     const uint8_t* zr[R];
@@ -181,25 +201,34 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
         sr[r] = s + n * p.lds;
         zr[r] = Z ? z + n * p.ldz : nullptr;
     }
-    const int first = wave * p.steps / kWaves, last = (wave + 1) * p.steps / kWaves;
     constexpr uint32_t kOne = F16 ? 0x3C003C00u : 0x3F803F80u;
     const u32x4 ones{kOne, kOne, kOne, kOne};
+    const Codes<F16> codes;
 
     for (int m0 = lo; m0 < hi; m0 += stride) {
-        // the row of x of operand row n16 of each block of tokens: token n16 / 4 + 4 (n16 % 4)
+        // the row of x of operand row n16 of each block of tokens: token n16 / 4 + 4 (n16 % 4);
+        // operand rows without a token repeat a token's, and their results are never stored
         const uint16_t* xr[MT];
-        bool live[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const int i = n16 & 3;
-            const int m = m0 + 16 * t + (n16 >> 2) + 4 * i;
-            live[t] = i < NI && m < hi;
-            int64_t row = m;
-            if (p.src && live[t])
-                row = p.src[m] / p.topk;
-            live[t] = live[t] && row >= 0 && row < p.x_rows;
-            xr[t] = p.x + (live[t] ? row : 0) * p.ldx;
+            const int m = m0 + 16 * t + (n16 >> 2) + 4 * ((n16 & 3) % NI);
+            xr[t] = p.x + x_row(p, min(m, hi - 1)) * p.ldx;
         }
+        const auto load = [&](Buf<G, Z, MT, R>& b, int unit) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                load_unit<G, Z, Tail>(b.w[r], cr[r], sr[r], zr[r], unit, g, p.K);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int col = unit * kUnit + 32 * j + 8 * g;
+                    b.x[t][j] = ld16(xr[t] + (Tail ? min(col, p.K - 8) : col));
+                }
+            }
+            // left alone, the compiler gathers the loads of all D units behind the last product
+            __builtin_amdgcn_sched_barrier(0);
+        };
         float sum[R][MT][NI];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -209,16 +238,15 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
                 for (int i = 0; i < NI; ++i)
                     sum[r][t][i] = 0.0f;
 
-        for (int k = first; k < last; ++k) {
-            Step<G, Z> st[R];
+        const auto compute = [&](Buf<G, Z, MT, R>& b, int unit) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                load_step<G, Z>(st[r], cr[r], sr[r], zr[r], k, g, p.K);
-                regroup<G>(st[r].q);
+                b.w[r].q[0] = exchange(b.w[r].q[0]);
+                b.w[r].q[1] = exchange(b.w[r].q[1]);
             }
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
-                if (gr > 0 && k * kTK + gr * G >= p.K)   // a last step of fewer groups
+                if (Tail && gr > 0 && unit * kUnit + gr * G >= p.K)
                     break;
                 f32x4 xs[MT], acc[R][MT];
 #pragma unroll
@@ -230,16 +258,13 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
                 }
 #pragma unroll
                 for (int j = gr * kPer; j < (gr + 1) * kPer; ++j) {
-                    const int col = k * kTK + col_of<G>(j, g);
                     u32x4 w[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        w[r] = operands<F16>(st[r].q[j]);
+                        w[r] = codes.operands(b.w[r].q[j >> 2][j & 3]);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        u32x4 x{};
-                        if (live[t] && col < p.K)
-                            x = in_order(ld16(xr[t] + col));
+                        const u32x4 x = in_order(b.x[t][j]);
                         xs[t] = mma<F16>(x, ones, xs[t]);
 #pragma unroll
                         for (int r = 0; r < R; ++r)
@@ -248,10 +273,10 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float scale = to_f32<F16>(st[r].s[gr]);
+                    const float scale = to_f32<F16>(b.w[r].s[gr / 2] >> (16 * (gr & 1)));
                     float zero = 24.0f;
                     if constexpr (Z)
-                        zero = 16.0f + (float)((st[r].z >> (8 * gr)) & 15u);
+                        zero = 16.0f + (float)((b.w[r].z[gr / 4] >> (8 * (gr & 3))) & 15u);
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -260,6 +285,45 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
                                 scale, __builtin_fmaf(-zero, xs[t][i], acc[r][t][i]), sum[r][t][i]);
                 }
             }
+            // The sums stay in this block of instructions: the compiler has moved them behind the
+            // branch that follows, where a path reached them before the matrix instructions'
+            // results may be read (seen as wrong sums in binary16, group 128, one step of columns per wave).
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        asm volatile("" : "+v"(sum[r][t][i]));
+            __builtin_amdgcn_sched_barrier(0);
+        };
+
+        // D units are in flight.  The main loop has no branches, so that a unit waits for its own
+        // loads only; the last 2 D - 1 units at most are taken one by one.
+        if (wave < p.units) {
+            Buf<G, Z, MT, R> buf[D];
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                load(buf[d], min(wave + d * KW, p.units - 1));
+            int k = wave;
+            for (; k + (2 * D - 1) * KW < p.units; k += D * KW) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    compute(buf[d], k + d * KW);
+                    load(buf[d], k + (d + D) * KW);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (k + d * KW < p.units)
+                    compute(buf[d], k + d * KW);
+                if (k + (d + D) * KW < p.units)
+                    load(buf[d], k + (d + D) * KW);
+            }
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                if (k + (d + D) * KW < p.units)
+                    compute(buf[d], k + (d + D) * KW);
         }
 
 #pragma unroll
@@ -270,45 +334,484 @@ __global__ __launch_bounds__(kThreads) void k_mv_i4(Args p) {
                 for (int i = 0; i < NI; ++i)
                     red[wave][(r * MT + t) * NI + i][lane] = sum[r][t][i];
         __syncthreads();
-        for (int u = wave; u < R * MT * NI; u += kWaves) {
+        for (int u = wave; u < R * MT * NI; u += KW) {
             float v = red[0][u][lane];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < KW; ++w)
                 v += red[w][u][lane];
             const int i = u % NI, t = u / NI % MT, r = u / (NI * MT);
             const int m = m0 + 16 * t + g + 4 * i, n = n0 + 16 * r + n16;
             if (m < hi && n < p.N)
-                p.y[m * p.ldy + n] = from_f32<F16>(v);
+                p.y[m * p.ldy + n] = from_f32<F16>(x_row_ok(p, m) ? v : 0.0f);
         }
         __syncthreads();
     }
 }
 
-template <bool F16, int G, bool Z, int NI, int MT, int R>
+// ---- many rows ------------------------------------------------------------------------------
+//
+// With many rows of x the matrix cores bound the work.  A workgroup of 4 waves computes TM rows
+// of x (128, or 64 where there are fewer) by 256 rows of W; a wave all TM by 64.  Stages
+// of 64 columns go through LDS, x and codes both, brought there by global-to-LDS loads in a
+// ring of three: while a stage is computed, the next one has landed or is landing and the one
+// after it is being fetched.  Scales and zero points come for several stages (a unit) at once.
+// Per stage a wave turns its 64 x 64 codes into operands once and uses them for all blocks of 16
+// rows of x; each group's products start from zero and are multiplied by the scale into the
+// running sums, in registers.
+
+constexpr int kTN = 256, kStage = 64;
+constexpr int kTileThreads = 256, kTileWaves = 4;
+constexpr int kWaveN = kTN / kTileWaves, kNB = kWaveN / 16;
+constexpr int kRing = 3;
+constexpr int64_t kMaxGridY = 65535;
+
+template <int TM>
+struct alignas(16) TileStage {
+    uint8_t x[TM * 128];     // rows of 8 chunks of 16 bytes; chunk c of row r in slot c ^ (r & 7)
+    uint8_t w[kTN * 32];     // rows of 32 bytes of codes
+};
+
+template <int G, bool Z, bool F16, int TM>
+struct alignas(16) TileShared {
+    static constexpr int kUnit = G == 32 ? 128 : 256;    // columns whose scales come together
+    static constexpr int kS = kUnit / G / 2;             // words of scales of a row and unit
+    TileStage<TM> stage[kRing];
+    uint32_t s[2][kTN * kS];
+    uint32_t z[Z ? 2 : 1][Z ? kTN : 1];                  // one word of zero points
+    alignas(16) float xs[F16 ? 4 : 2 * TM];              // sums of x per row and half stage
+};
+// two workgroups of 128 rows fit a compute unit's 160 KB
+static_assert(sizeof(TileShared<32, true, false, 128>) <= 80 * 1024, "LDS of a workgroup");
+
+// Global-to-LDS load of 16 (4) bytes per lane: lane i's land at lds + 16 i (4 i).
+__device__ __forceinline__ void lds_load16(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
+}
+// Until at most N of this wave's loads are outstanding, and then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_join() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The 8 codes of a word as operands in column order, less the zero point where the type has
+// a packed subtraction.  Codes 2i, 2i+1 are byte i of the even and of the odd nibbles.
+//  bf16: 16 + code.  The code's bits sit in the low byte under a set bit 7; the high byte is
+//        0x41 (16.0 is 0x4180).
+//  binary16: (code - zero) / 512, exactly.  A byte by itself is the subnormal code * 2^-24; one
+//        packed fused multiply-add by 2^15 makes it normal and subtracts the zero point.
+template <bool F16>
+struct TileCodes {
+    uint32_t mask, set, high;
+    __device__ __forceinline__ TileCodes()
+        : mask(F16 ? 0x0F0F0F0Fu : 0x78787878u), set(0x80808080u), high(0x41414141u) {
+        asm("" : "+s"(mask));
+        asm("" : "+v"(set));
+        asm("" : "+s"(high));
+    }
+    __device__ __forceinline__ u32x4 operands(uint32_t w, h16x2 less) const {
+        u32x4 r;
+        if constexpr (F16) {
+            const uint32_t e = w & mask, o = (w >> 4) & mask;
+            const h16x2 up{(_Float16)32768.0f, (_Float16)32768.0f};
+            constexpr uint32_t sel[4] = {0x0C040C00u, 0x0C050C01u, 0x0C060C02u, 0x0C070C03u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const h16x2 c = __builtin_bit_cast(h16x2, __builtin_amdgcn_perm(o, e, sel[i]));
+                r[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, up, less));
+            }
+        } else {
+            const uint32_t e = ((w << 3) & mask) | set, o = ((w >> 1) & mask) | set;
+            const uint32_t lo = __builtin_amdgcn_perm(o, e, 0x05010400u);   // codes 0 1 2 3
+            const uint32_t hi = __builtin_amdgcn_perm(o, e, 0x07030602u);   // codes 4 5 6 7
+            r[0] = __builtin_amdgcn_perm(high, lo, 0x04010400u);
+            r[1] = __builtin_amdgcn_perm(high, lo, 0x04030402u);
+            r[2] = __builtin_amdgcn_perm(high, hi, 0x04010400u);
+            r[3] = __builtin_amdgcn_perm(high, hi, 0x04030402u);
+        }
+        return r;
+    }
+};
+
+// The expert and the first row of row block `block`, blocks counted expert by expert; -1 for one
+// past the last.
+template <int TM>
+__device__ __forceinline__ int find_block(const Args& p, int block, int& lo, int& hi) {
+    if (!p.off) {
+        lo = block * TM;
+        hi = p.rows;
+        return lo < hi ? 0 : -1;
+    }
+    const int lane = threadIdx.x & 63;
+    int seen = 0;
+    for (int base = 0; base < p.experts; base += 64) {
+        const int e = base + lane;
+        int first = 0, end = 0;
+        if (e < p.experts) {
+            first = max(p.off[e], 0);
+            end = min(p.off[e + 1], p.rows);
+        }
+        const int mine = max(end - first + TM - 1, 0) / TM;
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(inc, d);
+            inc += lane >= d ? o : 0;
+        }
+        const uint64_t past = __ballot(seen + inc > block);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            lo = __shfl(first, l) + (block - seen - __shfl(inc - mine, l)) * TM;
+            hi = __shfl(end, l);
+            return base + l;
+        }
+        seen += __shfl(inc, 63);
+    }
+    return -1;
+}
+
+template <bool F16, int G, bool Z, int TM>
+__global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
+    using Shared = TileShared<G, Z, F16, TM>;
+    using Stage = TileStage<TM>;
+    constexpr int kMB = TM / 16, kXLoads = TM / 32;
+    __shared__ Shared sm;
+    const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lo, hi;
+    const int expert =
+        __builtin_amdgcn_readfirstlane(find_block<TM>(p, p.block0 + blockIdx.y, lo, hi));
+    if (expert < 0)
+        return;
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(min(hi, lo + TM));
+    const int n0 = blockIdx.x * kTN;
+    const uint8_t* c = p.c + expert * p.stride_c;
+    const uint16_t* s = p.s + expert * p.stride_s;
+    const uint8_t* z = Z ? p.z + expert * p.stride_z : nullptr;
+
+    // what this thread brings: x rows tid / 8 + 32 i, chunk tid % 8 (of the slot's row); codes of
+    // rows tid / 2 + 128 i, half tid % 2
+    const uint16_t* xp[kXLoads];
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+        const int r = (tid >> 3) + 32 * i;
+        xp[i] = p.x + x_row(p, min(lo + r, hi - 1)) * p.ldx;
+    }
+    const int xc = 8 * ((tid & 7) ^ ((tid >> 3) & 7));
+    const uint8_t* cp[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        cp[i] = c + min(n0 + (tid >> 1) + 128 * i, p.N - 1) * p.ldc;
+    const int stages = (p.K + kStage - 1) / kStage;
+    const auto issue = [&](int stage, int slot) {
+        Stage& t = sm.stage[slot];
+        const int k = stage * kStage;
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i)
+            lds_load16(xp[i] + min(k + xc, p.K - 8), t.x + wave * 1024 + i * 4096);
+        const int kc = min(k + 32 * (tid & 1), p.K - 32) / 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            lds_load16(cp[i] + kc, t.w + wave * 1024 + i * 4096);
+    };
+    // a wave's own 64 rows of scales and zero points, word by word
+    constexpr int kS = Shared::kS, kUnitGroups = Shared::kUnit / G;
+    const int groups = p.K / G;
+    const auto issue_scales = [&](int unit) {
+        int l = lane;
+        asm volatile("" : "+v"(l));     // addresses are made anew: registers are short
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+            const int row = min(n0 + wave * kWaveN + i * (64 / kS) + l / kS, p.N - 1);
+            const int at = min(unit * kUnitGroups + 2 * (l % kS), (groups - 1) & ~1);
+            lds_load4(s + row * p.lds + at, &sm.s[unit & 1][(wave * kWaveN + i * (64 / kS)) * kS]);
+        }
+        if constexpr (Z) {
+            const int row = min(n0 + wave * kWaveN + l, p.N - 1);
+            const int at = min(unit * kUnitGroups, groups - 1) & ~3;
+            lds_load4(z + row * p.ldz + at, &sm.z[unit & 1][wave * kWaveN]);
+        }
+    };
+    constexpr int kStageLoads = kXLoads + 2, kScaleLoads = kS + (Z ? 1 : 0);
+
+    f32x4 sum[kMB][kNB];
+#pragma unroll
+    for (int t = 0; t < kMB; ++t)
+#pragma unroll
+        for (int b = 0; b < kNB; ++b)
+            sum[t][b] = f32x4{};
+    const TileCodes<F16> codes;
+    constexpr int kHalves = G == 32 ? 2 : 1;    // groups of a stage
+
+    // the chunk of a row of x that feeds matrix instruction j: a lane quarter's 16 codes are
+    // columns [16 g, 16 g + 16), traded between the halves of the wave where a group has 32
+    const auto chunk = [&](int j) {
+        return G == 32 ? 4 * j + ((g & 1) << 1 | g >> 1) : 2 * g + j;
+    };
+    const auto x_at = [&](const Stage& t, int block, int j) {
+        const int r = 16 * block + n16;
+        return *reinterpret_cast<const u32x4*>(t.x + r * 128 + 16 * (chunk(j) ^ (r & 7)));
+    };
+    // bf16: the sums of x per row and group of a stage, each wave its share of the blocks of rows
+    // (negative, and times the 24 of the constant zero point, where the products start from them)
+    const auto sums_of_x = [&](const Stage& t) {
+        const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        for (int block = wave; block < kMB; block += kTileWaves) {
+            f32x4 a = mma<F16>(x_at(t, block, 0), ones, f32x4{});
+            f32x4 b = mma<F16>(x_at(t, block, 1), ones, kHalves == 2 ? f32x4{} : a);
+            a *= Z ? -1.0f : -24.0f;
+            b *= Z ? -1.0f : -24.0f;
+            asm volatile("" : "+v"(a), "+v"(b));    // before the branch (see k_mv_i4)
+            if (n16 == 0) {
+                float* xs = sm.xs + 16 * block + 4 * g;
+                *reinterpret_cast<f32x4*>(xs) = kHalves == 2 ? a : b;
+                if (kHalves == 2)
+                    *reinterpret_cast<f32x4*>(xs + TM) = b;
+            }
+        }
+    };
+    const auto compute = [&](int stage, int q, int slot, int unit) {
+        const Stage& t = sm.stage[slot];
+        // everything the operands are made of is read first, and block 0 of x
+        u32x2 raw[kNB];
+        uint32_t sw[kNB], zw[kNB];
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+            const int row = wave * kWaveN + 16 * b + n16;
+            raw[b] = *reinterpret_cast<const u32x2*>(t.w + row * 32 + 8 * g);
+            // the word with this stage's group (or its two)
+            sw[b] = sm.s[unit & 1][row * kS + (G == 128 ? 0 : G == 64 ? q / 2 : q)];
+            if constexpr (Z)
+                zw[b] = sm.z[unit & 1][row];
+        }
+        if constexpr (!F16)
+            sums_of_x(t);
+        // bf16 with zero points has no registers for two blocks (a spill would wait for the loads
+        // of later stages): its next operand is read when the last one has been used
+        constexpr int kXBufs = !F16 && Z ? 1 : 2;
+        u32x4 x[kXBufs][2];
+        x[0][0] = x_at(t, 0, 0);
+        x[0][1] = x_at(t, 0, 1);
+        u32x4 w[kNB][2];
+        float scale[kNB][kHalves], zero[kNB][kHalves];
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+            if constexpr (G == 32) {
+                const auto v = __builtin_amdgcn_permlane32_swap(raw[b].x, raw[b].y, false, false);
+                raw[b] = u32x2{v[0], v[1]};
+            }
+            h16x2 less[kHalves];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                const int half = G == 128 ? q / 2 : G == 64 ? q & 1 : h;    // of the word
+                scale[b][h] = to_f32<F16>(sw[b] >> (16 * half));
+                if (h == 1 && stage * kStage + 32 >= p.K)   // half a last stage
+                    scale[b][h] = 0.0f;
+                zero[b][h] = 8.0f;
+                if constexpr (Z) {
+                    const int byte = G == 128 ? 2 * (unit & 1) + q / 2 : G == 64 ? q : 2 * q + h;
+                    zero[b][h] = (float)((zw[b] >> (8 * byte)) & 15u);
+                }
+                if constexpr (F16) {
+                    scale[b][h] *= 512.0f;
+                    const _Float16 l = (_Float16)(zero[b][h] * (-1.0f / 512.0f));
+                    less[h] = h16x2{l, l};
+                } else {
+                    less[h] = h16x2{};
+                    zero[b][h] += 16.0f;
+                }
+            }
+            w[b][0] = codes.operands(raw[b].x, less[0]);
+            w[b][1] = codes.operands(raw[b].y, less[kHalves - 1]);
+        }
+        if constexpr (!F16)     // the other waves' sums of x
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+        // A step is one block of rows of x, or one group of it where a stage has two.  Its products
+        // run on the matrix cores while the vector units scale the step before and the next
+        // block of x comes from LDS: slots of one matrix instruction and its share of the
+        // scaling, held in this order.
+        constexpr int kSlots = 2 * kNB / kHalves, kSteps = kMB * kHalves;
+        f32x4 acc[2][kNB], xs[kXBufs];
+        const auto fold = [&](int step, int part) {
+            const int m = step / kHalves, h = step % kHalves;
+#pragma unroll
+            for (int e = part * 16 / kSlots; e < (part + 1) * 16 / kSlots; ++e) {
+                const int b = e / 4, i = e % 4;
+                float v = acc[step & 1][b][i];
+                if constexpr (!F16 && Z)
+                    v = __builtin_fmaf(zero[b][h], xs[0][i], v);
+                sum[m][b][i] = __builtin_fmaf(scale[b][h], v, sum[m][b][i]);
+            }
+        };
+        const auto read_xs = [&](int step) {
+            if constexpr (!F16)
+                xs[step % kXBufs] = *reinterpret_cast<const f32x4*>(sm.xs + (step % kHalves) * TM +
+                                                               16 * (step / kHalves) + 4 * g);
+        };
+        if constexpr (!F16 && !Z)
+            read_xs(0);
+#pragma unroll
+        for (int step = 0; step < kSteps; ++step) {
+            const int m = step / kHalves, h = step % kHalves;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const int b = i % kNB, j = kHalves == 2 ? h : i / kNB;
+                f32x4 from{};
+                if (i >= kNB)
+                    from = acc[step & 1][b];
+                else if (!F16 && !Z)
+                    from = xs[step % kXBufs];
+                acc[step & 1][b] = mma<F16>(x[m % kXBufs][j], w[b][j], from);
+                if constexpr (kXBufs == 2) {
+                    if (i == 0 && h == 0 && m + 1 < kMB) {
+                        x[(m + 1) & 1][0] = x_at(t, m + 1, 0);
+                        x[(m + 1) & 1][1] = x_at(t, m + 1, 1);
+                    }
+                    if (i == kSlots - 1 && step + 1 < kSteps)
+                        read_xs(step + 1);     // over those of the step before
+                } else {
+                    if (b == kNB - 1 && m + 1 < kMB)
+                        x[0][j] = x_at(t, m + 1, j);
+                }
+                if (step > 0)
+                    fold(step - 1, i);
+                if (kXBufs == 1 && i == kSlots - 1)
+                    read_xs(step);         // for the scaling of this step, in the next
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            fold(kSteps - 1, i);
+        // the sums stay in this block of instructions (see k_mv_i4)
+#pragma unroll
+        for (int m = 0; m < kMB; ++m)
+#pragma unroll
+            for (int b = 0; b < kNB; ++b)
+                asm volatile("" : "+v"(sum[m][b]));
+    };
+
+    issue_scales(0);
+    issue(0, 0);
+    issue(min(1, stages - 1), 1);
+    wait_and_join<0>();
+    int slot = 0;
+    constexpr int kUnitStages = Shared::kUnit / kStage;
+    for (int unit = 0; unit * kUnitStages < stages; ++unit) {
+#pragma unroll
+        for (int q = 0; q < kUnitStages; ++q) {
+            const int stage = unit * kUnitStages + q;
+            const int next = slot == kRing - 1 ? 0 : slot + 1;
+            issue(min(stage + 2, stages - 1), next == kRing - 1 ? 0 : next + 1);
+            if (q == 0)
+                issue_scales(unit + 1);
+            if (stage < stages)
+                compute(stage, q, slot, unit);
+            // the next stage has landed when only what this one issued is outstanding
+            if (q == 0)
+                wait_and_join<kStageLoads + kScaleLoads>();
+            else
+                wait_and_join<kStageLoads>();
+            slot = next;
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands in LDS after the end
+
+#pragma unroll
+    for (int m = 0; m < kMB; ++m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = lo + 16 * m + 4 * g + i;
+            if (row < hi) {
+                const bool ok = x_row_ok(p, row);
+#pragma unroll
+                for (int b = 0; b < kNB; ++b) {
+                    const int n = n0 + wave * kWaveN + 16 * b + n16;
+                    if (n < p.N)
+                        p.y[row * p.ldy + n] = from_f32<F16>(ok ? sum[m][b][i] : 0.0f);
+                }
+            }
+        }
+    }
+}
+
+template <bool F16, int G, bool Z, int TM>
+hipError_t launch_tile(const Args& a0, hipStream_t st) {
+    Args a = a0;
+    // experts: every expert's last block may be partial
+    const int64_t blocks = a.off ? a.rows / TM + a.experts : (a.rows + TM - 1) / TM;
+    hipError_t e = hipSuccess;
+    for (int64_t b = 0; b < blocks && e == hipSuccess; b += kMaxGridY) {
+        a.block0 = (int32_t)b;
+        const int64_t n = blocks - b < kMaxGridY ? blocks - b : kMaxGridY;
+        const dim3 grid((unsigned)((a.N + kTN - 1) / kTN), (unsigned)n);
+        e = launch1(k_mm_i4<F16, G, Z, TM>, grid, dim3(kTileThreads), st, a);
+    }
+    return e;
+}
+
+template <bool F16, int G, bool Z, bool Tail, int NI, int MT, int R, int KW, int D>
 hipError_t launch_mv(const Args& a0, hipStream_t st) {
     Args a = a0;
-    constexpr int kTokens = MT == 1 ? 4 * NI : 16 * MT;
+    constexpr int kTokens = 16 * (MT - 1) + 4 * NI;
     const int64_t chunks = ((int64_t)a.rows + kTokens - 1) / kTokens;
     a.chunk = (int32_t)(chunks < 16384 ? chunks : 16384);
     const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), a.off ? a.experts : a.chunk);
-    return launch1(k_mv_i4<F16, G, Z, NI, MT, R>, grid, dim3(kThreads), st, a);
+    return launch1(k_mv_i4<F16, G, Z, Tail, NI, MT, R, KW, D>, grid, dim3(64 * KW), st, a);
 }
 
-template <bool F16, int G, bool Z>
-hipError_t launch_rows(const Args& a, hipStream_t st) {
-    const int64_t m = a.off ? (a.rows + a.experts - 1) / a.experts : a.rows;
+// The kernel for few rows.  Rules and measurements on MI355X (bf16, group 128, us):
+//  - Up to 4 rows take one result per lane, up to 16 four, and above blocks of 16 tokens: two up
+//    to 32 rows (32 x 7168 x 7168: 19.9 against 24.8 with four blocks), else four.
+//  - Two blocks of weight rows share the operands of x (16 x 7168 x 43008, group 64 with zero
+//    points: 76 against 110 with one).  Where that makes fewer workgroups than half the compute
+//    units, one block each (1 x 1024 x 43008: 25.8 against 38.7).
+//  - By expert there are workgroups enough for four blocks (8 rows for each of 64 experts of
+//    4096 x 7168: 254 against 283 with two) where they are still two per unit.
+template <bool F16, int G, bool Z, bool Tail>
+hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
+    if (a.off) {
+        if ((int64_t)a.experts * (a.N / 64) >= 512)
+            return launch_mv<F16, G, Z, Tail, 4, 1, 4, 4, 1>(a, st);
+        return launch_mv<F16, G, Z, Tail, 4, 1, 2, 4, 1>(a, st);
+    }
+    const bool narrow = a.N < 4096;
     if (m <= 4)
-        return launch_mv<F16, G, Z, 1, 1, 1>(a, st);
-    if (m <= 8)
-        return launch_mv<F16, G, Z, 2, 1, 1>(a, st);
+        return narrow ? launch_mv<F16, G, Z, Tail, 1, 1, 1, 8, 2>(a, st)
+                      : launch_mv<F16, G, Z, Tail, 1, 1, 2, 8, 1>(a, st);
     if (m <= 16)
-        return launch_mv<F16, G, Z, 4, 1, 2>(a, st);
-    return launch_mv<F16, G, Z, 4, 4, 2>(a, st);
+        return narrow ? launch_mv<F16, G, Z, Tail, 4, 1, 1, 8, 1>(a, st)
+                      : launch_mv<F16, G, Z, Tail, 4, 1, 2, 8, 1>(a, st);
+    if (m <= 32)
+        return launch_mv<F16, G, Z, Tail, 4, 2, 2, 4, 1>(a, st);
+    return launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);
+}
+
+// Few rows or many (us, bf16, group 128, 7168 x 7168): 192 rows 97 with the kernel for few
+// against 107 with the one for many, 256 rows 128 against 108.  By expert the kernel for many
+// wins from 16 rows an expert (64 experts of 4096 x 7168: 349 against 350 there, 403 against
+// 837 at 32).  Tiles of 128 rows where they make workgroups enough: 2048 rows 248 against
+// 297 with tiles of 64, 1024 rows 171 against 161; by expert 96 rows 684 against 668, 160 rows
+// 964 against 986.
+template <bool F16, int G, bool Z>
+hipError_t launch_shape(const Args& a, hipStream_t st) {
+    const int64_t m = a.off ? (a.rows + a.experts - 1) / a.experts : a.rows;
+    if (m > (a.off ? 16 : 192)) {
+        const int64_t tiles = (m + 127) / 128 * ((a.N + kTN - 1) / kTN);
+        const bool tall = a.off ? m > 128 : tiles >= 384;
+        return tall ? launch_tile<F16, G, Z, 128>(a, st) : launch_tile<F16, G, Z, 64>(a, st);
+    }
+    return a.K % kUnit != 0 ? launch_few<F16, G, Z, true>(a, m, st)
+                            : launch_few<F16, G, Z, false>(a, m, st);
 }
 
 template <bool F16, int G>
 hipError_t launch_zero(const Args& a, hipStream_t st) {
-    return a.z ? launch_rows<F16, G, true>(a, st) : launch_rows<F16, G, false>(a, st);
+    return a.z ? launch_shape<F16, G, true>(a, st) : launch_shape<F16, G, false>(a, st);
 }
 
 }  // namespace
@@ -316,7 +819,7 @@ hipError_t launch_zero(const Args& a, hipStream_t st) {
 hipError_t launch_mm_i4(const I4Mm& m, int group, bool f16, hipStream_t stream) {
     Args a{};
     static_cast<I4Mm&>(a) = m;
-    a.steps = (a.K + kTK - 1) / kTK;
+    a.units = (a.K + kUnit - 1) / kUnit;
     if (f16)
         return group == 32 ? launch_zero<true, 32>(a, stream)
              : group == 64 ? launch_zero<true, 64>(a, stream)

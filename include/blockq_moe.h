@@ -31,8 +31,8 @@ extern "C" {
  * W[n][k] = (code - zero) * scale.  group is 32, 64 or 128 and K a multiple of it.
  * Layout rules: c 16-byte aligned, ldc >= K/2, ldc % 16 == 0; scale 8-byte aligned, lds >=
  * K/group, lds % 4 == 0; zero 4-byte aligned, ldz >= K/group, ldz % 4 == 0.  Scale and zero
- * rows are read in whole units of 128 columns, so the entries after the last group, up to
- * the next multiple of 128/group, must be readable (they are not used). */
+ * rows are read in whole fours of entries, so the entries after the last group, up to the
+ * next multiple of 4, must be readable (they are not used). */
 
 /* bf16 rows -> I4 codes and scales, symmetric (zero point 8).  Per group: amax = max |x|;
  * scale = bf16_rne(fl32(amax / 7)); code = 8 + q, q = round-half-even(fl32(x / scale))
