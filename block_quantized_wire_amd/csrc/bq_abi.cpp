@@ -1024,6 +1024,7 @@ bq_status bq_mm_i4_f16(const uint16_t* x, int64_t ldx, const uint8_t* c, int64_t
 namespace {
 
 constexpr int64_t kMaxSlots = (int64_t)1 << 30;
+constexpr int64_t kMaxCols = (int64_t)1 << 22;    // 2^20 units of 16 bytes in a row
 
 bq_status check_moe(int64_t tokens, int topk, int experts) {
     if (topk < 1 || topk > BQ_MAX_TOPK || experts < 1 || experts > BQ_MAX_EXPERTS)
@@ -1035,7 +1036,7 @@ bq_status check_moe(int64_t tokens, int topk, int experts) {
 
 // pos and off, which every call on rows reads, and the column count.
 bq_status check_moe_rows(const bq::MoeRows& r) {
-    if (r.cols < 0 || r.cols > kI4MaxDim)
+    if (r.cols < 0 || r.cols > kMaxCols)
         return BQ_ERR_SIZE;
     return BQ_OK;
 }

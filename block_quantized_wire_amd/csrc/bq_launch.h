@@ -125,7 +125,7 @@ hipError_t launch_mm_i4(const I4Mm& a, int group, bool f16, hipStream_t stream);
 // Tokens sorted by expert.  Sorts of up to kMoeSortOneBlock slots take one workgroup and no
 // scratch, larger ones at most kMoeSortBlocks workgroups and one count per bucket and
 // workgroup.
-constexpr int64_t kMoeSortOneBlock = 8192;
+constexpr int64_t kMoeSortOneBlock = 4096;
 constexpr int64_t kMoeSortBlocks = 256;
 hipError_t launch_moe_sort(const int32_t* expert, int64_t slots, int experts, int32_t* off,
                            int32_t* src, int32_t* pos, void* ws, hipStream_t stream);

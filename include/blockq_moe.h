@@ -80,13 +80,13 @@ bq_status bq_mm_i4_f16(const uint16_t* x, int64_t ldx, const uint8_t* c, int64_t
  *   off[experts + 1]: rows [off[e], off[e+1]) belong to expert e; off[experts] rows are kept;
  *   src[tokens*topk]: the slot in each row;   pos[tokens*topk]: the row of each slot.
  * 1 <= topk <= BQ_MAX_TOPK, 1 <= experts <= BQ_MAX_EXPERTS (else BQ_ERR_NSRC); tokens * topk
- * < 2^30 (else BQ_ERR_SIZE).  Entries of the arrays that are out of range (arrays not made
+ * < 2^30 and at most 2^22 columns in a row that is moved (else BQ_ERR_SIZE).  Entries of the arrays that are out of range (arrays not made
  * by bq_moe_sort) are never used as addresses: rows past the arrays' ends are skipped.
  * int32 and float arrays are 4-byte aligned. */
 #define BQ_MAX_TOPK 64
 #define BQ_MAX_EXPERTS 1024
 
-/* Scratch bytes of bq_moe_sort: 0 up to 8192 slots, else 1024 * (experts + 1).  Returns -1
+/* Scratch bytes of bq_moe_sort: 0 up to 4096 slots, else 1024 * (experts + 1).  Returns -1
  * for sizes outside the limits. */
 int64_t bq_moe_sort_ws_bytes(int64_t tokens, int topk, int experts);
 

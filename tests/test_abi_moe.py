@@ -194,9 +194,9 @@ def test_sort_refusals():
     for k in ("off", "src", "pos", "ws"):
         refuse(call, ALIAS, **{k: SORT["expert"] + 400})
     refuse(call, ALIAS, src=at(4))
-    assert bq.bq_moe_sort_ws_bytes(8192, 1, 8) == 0
-    assert bq.bq_moe_sort_ws_bytes(1024, 8, 1024) == 0
-    assert bq.bq_moe_sort_ws_bytes(8193, 1, 8) == 1024 * 9
+    assert bq.bq_moe_sort_ws_bytes(4096, 1, 8) == 0
+    assert bq.bq_moe_sort_ws_bytes(512, 8, 1024) == 0
+    assert bq.bq_moe_sort_ws_bytes(4097, 1, 8) == 1024 * 9
     for bad in ((-1, 1, 8), (1, 0, 8), (1, 1, 0), (1, 65, 8), (1, 1, 1025), (1 << 30, 1, 8)):
         assert bq.bq_moe_sort_ws_bytes(*bad) == -1
 

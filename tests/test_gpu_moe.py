@@ -45,7 +45,7 @@ def sort_on_gpu(ids, experts, stream=None):
 @pytest.mark.parametrize("tokens,topk,experts,drop", [
     (1, 1, 1, 0.0), (1, 1, 1, 1.0), (1, 8, 256, 0.0), (3, 2, 5, 0.3), (63, 1, 4, 0.0),
     (64, 1, 4, 0.1), (65, 1, 1024, 0.0), (511, 1, 2, 0.5), (512, 1, 1, 0.0), (513, 3, 511, 0.1),
-    (1024, 8, 512, 0.0), (8193, 1, 7, 0.2), (1025, 8, 64, 0.0), (4097, 6, 48, 0.125),
+    (512, 8, 512, 0.0), (4097, 1, 7, 0.2), (1024, 8, 512, 0.0), (8193, 1, 7, 0.2), (1025, 8, 64, 0.0), (4097, 6, 48, 0.125),
     (20000, 8, 256, 0.0), (20000, 8, 1024, 0.5), (70000, 64, 3, 0.1), (300, 64, 513, 0.0),
 ])
 def test_sort(tokens, topk, experts, drop):
