@@ -7,7 +7,12 @@
 // they are: a pair of codes becomes a pair of matrix operands with one shift and one
 // and-or.  Both sums run on the matrix cores in binary32 (sum x as a product with ones), and
 // the group's scale multiplies their difference once, in binary32.  The offset of 16 costs
-// at most a factor of 16 + zero over |code - zero| in the rounding of binary32 sums.
+// at most a factor of 16 + zero over |code - zero| in the rounding of binary32 sums.  (bf16
+// has no packed subtraction; binary16 has, and k_mm_i4 subtracts the zero point there.)
+//
+// Three kernels, chosen by the row count (launch_shape): k_ms_i4 for up to 16 rows and k_mv_i4
+// for up to 192, bound by the bytes of the weights, and k_mm_i4, bound by the matrix cores
+// and the vector instructions that feed them.  Rates at a stated size stand at each.
 #include "bq_device.h"
 #include "bq_launch.h"
 
@@ -160,6 +165,19 @@ struct Buf {
     Weights<G, Z> w[R];
     u32x4 x[MT][8];
 };
+
+// Global-to-LDS load of 16 (4) bytes per lane: lane i's land at lds + 16 i (4 i).
+__device__ __forceinline__ void lds_load16(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
+}
+// Until at most N of this wave's loads are outstanding, and then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_join() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 // Few rows of x: the bytes of the weights bound this kernel, so it streams them once, straight
 // into registers, D units of 256 columns ahead.  A workgroup takes R blocks of 16 weight rows
@@ -359,6 +377,17 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // rows of x; each group's products start from zero and are multiplied by the scale into the
 // running sums, in registers.
 
+// Measured on MI355X (a large library product reaches 1400 TFLOP/s): 24594 sorted rows over 32
+// experts of 2048 x 7168, group 64 with zero points, 845 us in binary16 (854 TFLOP/s) and 1048
+// in bf16, whose zero points cost a second multiply-add for each result; group 128 without
+// 773 (934 TFLOP/s) and 917.  What bounds it are the instructions between the matrix
+// instructions: 264 vector and 64 matrix instructions a stage and wave, of which 128 scale
+// results and 88 make operands, with two waves to a SIMD.  Scaling the operands instead of the
+// results would save half of them and round every weight to 8 (11) bits, which it must not.
+// bf16's sums of x are made inside the stage, with a barrier of their own: made a stage ahead
+// they need a stage more in flight (1146 against 917 us).  Registers are short: a spilled one
+// is read back behind the stage's loads (531 against 689 TFLOP/s), so the scales' addresses are
+// made anew and bf16 with zero points holds one block of x instead of two.
 constexpr int kTN = 256, kStage = 64;
 constexpr int kTileThreads = 256, kTileWaves = 4;
 constexpr int kWaveN = kTN / kTileWaves, kNB = kWaveN / 16;
@@ -382,19 +411,6 @@ struct alignas(16) TileShared {
 };
 // two workgroups of 128 rows fit a compute unit's 160 KB
 static_assert(sizeof(TileShared<32, true, false, 128>) <= 80 * 1024, "LDS of a workgroup");
-
-// Global-to-LDS load of 16 (4) bytes per lane: lane i's land at lds + 16 i (4 i).
-__device__ __forceinline__ void lds_load16(const void* p, void* lds) {
-    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
-}
-__device__ __forceinline__ void lds_load4(const void* p, void* lds) {
-    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
-}
-// Until at most N of this wave's loads are outstanding, and then for the other waves.
-template <int N>
-__device__ __forceinline__ void wait_and_join() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 // The 8 codes of a word as operands in column order, less the zero point where the type has
 // a packed subtraction.  Codes 2i, 2i+1 are byte i of the even and of the odd nibbles.
@@ -764,14 +780,216 @@ hipError_t launch_mv(const Args& a0, hipStream_t st) {
     return launch1(k_mv_i4<F16, G, Z, Tail, NI, MT, R, KW, D>, grid, dim3(64 * KW), st, a);
 }
 
-// The kernel for few rows.  Rules and measurements on MI355X (bf16, group 128, us):
-//  - Up to 4 rows take one result per lane, up to 16 four, and above blocks of 16 tokens: two up
-//    to 32 rows (32 x 7168 x 7168: 19.9 against 24.8 with four blocks), else four.
-//  - Two blocks of weight rows share the operands of x (16 x 7168 x 43008, group 64 with zero
-//    points: 76 against 110 with one).  Where that makes fewer workgroups than half the compute
-//    units, one block each (1 x 1024 x 43008: 25.8 against 38.7).
-//  - By expert there are workgroups enough for four blocks (8 rows for each of 64 experts of
-//    4096 x 7168: 254 against 283 with two) where they are still two per unit.
+// ---- few rows, staged through LDS -----------------------------------------------------------
+//
+// The same sums as k_mv_i4's for up to 16 rows, with every byte brought to LDS by global-to-LDS
+// loads.  A matrix operand wants 16 different rows in 16 adjacent lanes, and a load in that
+// order touches 16 lines of memory for every 256 bytes; through LDS each load instruction reads
+// whole lines.  A wave keeps to itself: its own units of 256 columns, its own ring of D units,
+// no barriers until the sums meet.  4 NI rows of x (NI = 1, 2 or 4) at a time.
+// Measured at 16 x 7168 x 43008, group 64 with zero points (170 MB, 35 us at the rate of a large
+// copy): 57 us, against 76 with loads to registers.  Units of 128 columns, which leave room
+// for 8 waves, take 70 (runs of 64 bytes); pairs of waves that share a unit's x and meet at a
+// barrier for each 65; 16 rows of W 72, 64 rows 98.  Bound by the loads of x, 8 KB for 4 KB of
+// codes: one row of x takes 41 us (4.1 TB/s).
+template <int G, bool Z, int NI, int R>
+struct alignas(16) Staged {
+    static constexpr int kS = kUnit / G / 2;         // words of scales of a row and unit
+    static constexpr int kZ = G == 32 ? 2 : 1;       // words of zero points
+    static constexpr int kSLoads = (16 * R * kS + 63) / 64, kZLoads = Z ? (16 * R * kZ + 63) / 64 : 0;
+    uint8_t w[16 * R * 128];         // rows of 8 chunks of 16 bytes, chunk c in slot c ^ (row & 7)
+    uint8_t x[4 * NI * 512];         // rows of 32 chunks, chunk c in slot c ^ (row & 7)
+    uint32_t s[64 * kSLoads];
+    uint32_t z[Z ? 64 * kZLoads : 4];
+};
+
+template <bool F16, int G, bool Z, bool Tail, int NI, int R, int KW, int D>
+__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) void k_ms_i4(Args p) {
+    using St = Staged<G, Z, NI, R>;
+    constexpr int kGroups = kUnit / G, kPer = 8 / kGroups, kTokens = 4 * NI;
+    constexpr int kS = St::kS, kZ = St::kZ;
+    __shared__ St ring[KW][D];
+    static_assert(sizeof(St) * D >= R * NI * 64 * 4, "the sums fit a wave's ring");
+    const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16 * R;
+    const int groups = p.K / G;
+    constexpr uint32_t kOne = F16 ? 0x3C003C00u : 0x3F803F80u;
+    const u32x4 ones{kOne, kOne, kOne, kOne};
+    const Codes<F16> codes;
+    // Addresses are a uniform base that moves with the unit and a lane's 32-bit offset, which
+    // the launch has checked to be enough.  First what this lane brings of the weights.
+    uint32_t co[2 * R], so[St::kSLoads], zo[Z ? St::kZLoads : 1];
+    const uint32_t wk = 16 * ((lane & 7) ^ (lane >> 3));     // bytes of this lane's chunk
+    const int left_n = p.N - 1 - n0;
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i)
+        co[i] = (uint32_t)(min(8 * i + (lane >> 3), left_n) * p.ldc);
+#pragma unroll
+    for (int i = 0; i < St::kSLoads; ++i)
+        so[i] = (uint32_t)(min(min((64 * i + lane) / kS, 16 * R - 1), left_n) * p.lds);
+#pragma unroll
+    for (int i = 0; i < St::kZLoads; ++i)
+        zo[i] = (uint32_t)(min(min((64 * i + lane) / kZ, 16 * R - 1), left_n) * p.ldz);
+    const uint8_t* c0 = p.c + n0 * p.ldc;
+    const uint16_t* s0 = p.s + n0 * p.lds;
+    const uint8_t* z0 = Z ? p.z + n0 * p.ldz : nullptr;
+
+    for (int m0 = blockIdx.y * kTokens; m0 < p.rows; m0 += p.chunk * kTokens) {
+        uint32_t xo[2 * NI], xk[2 * NI];       // values
+#pragma unroll
+        for (int i = 0; i < 2 * NI; ++i) {
+            const int r = 2 * i + (lane >> 5);
+            xo[i] = (uint32_t)(min(r, p.rows - 1 - m0) * p.ldx);
+            xk[i] = 8 * ((lane & 31) ^ (r & 7));
+        }
+        const uint16_t* x0 = p.x + m0 * p.ldx;
+        const auto issue = [&](int unit, int slot) {
+            St& t = ring[wave][slot];
+            const uint32_t k = unit * kUnit, left = p.K - k;    // columns from here on
+            const uint8_t* cu = c0 + k / 2;
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i)
+                lds_load16(cu + (co[i] + (Tail ? min(wk, left / 2 - 16) : wk)), t.w + 1024 * i);
+            const uint16_t* xu = x0 + k;
+#pragma unroll
+            for (int i = 0; i < 2 * NI; ++i)
+                lds_load16(xu + (xo[i] + (Tail ? min(xk[i], left - 8) : xk[i])), t.x + 1024 * i);
+            // scales two to a word, zero points four; a word past the last group repeats its word
+            const uint32_t first = unit * kGroups, at4 = first & ~3u;
+            const uint32_t end2 = ((groups - 1) & ~1u) - first, end4 = ((groups - 1) & ~3u) - at4;
+            const uint16_t* su = s0 + first;
+#pragma unroll
+            for (int i = 0; i < St::kSLoads; ++i) {
+                const uint32_t w = 2 * ((64 * i + lane) % kS);
+                lds_load4(su + (so[i] + (Tail ? min(w, end2) : w)), t.s + 64 * i);
+            }
+            if constexpr (Z) {
+                const uint8_t* zu = z0 + at4;
+#pragma unroll
+                for (int i = 0; i < St::kZLoads; ++i) {
+                    const uint32_t w = 4 * ((64 * i + lane) % kZ);
+                    lds_load4(zu + (zo[i] + (Tail ? min(w, end4) : w)), t.z + 64 * i);
+                }
+            }
+        };
+        constexpr int kLoads = 2 * R + 2 * NI + St::kSLoads + St::kZLoads;
+
+        float sum[R][NI];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                sum[r][i] = 0.0f;
+        const auto compute = [&](int unit, int slot) {
+            const St& t = ring[wave][slot];
+            u32x4 q[R][2];
+            uint32_t sw[R][kS], zw[R][kZ];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = 16 * r + n16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    q[r][h] = exchange(*reinterpret_cast<const u32x4*>(
+                        t.w + row * 128 + 16 * ((4 * h + g) ^ (row & 7))));
+#pragma unroll
+                for (int i = 0; i < kS; ++i)
+                    sw[r][i] = t.s[row * kS + i];
+#pragma unroll
+                for (int i = 0; i < kZ; ++i)
+                    zw[r][i] = Z ? t.z[row * kZ + i] : 0;
+            }
+            const int xr = (n16 >> 2) + 4 * ((n16 & 3) % NI);   // the token of operand row n16
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                if (Tail && gr > 0 && unit * kUnit + gr * G >= p.K)
+                    break;
+                f32x4 xs{}, acc[R] = {};
+#pragma unroll
+                for (int j = gr * kPer; j < (gr + 1) * kPer; ++j) {
+                    const u32x4 x = in_order(*reinterpret_cast<const u32x4*>(
+                        t.x + xr * 512 + 16 * ((4 * j + g) ^ (xr & 7))));
+                    xs = mma<F16>(x, ones, xs);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        acc[r] = mma<F16>(x, codes.operands(q[r][j >> 2][j & 3]), acc[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float scale = to_f32<F16>(sw[r][gr / 2] >> (16 * (gr & 1)));
+                    float zero = 24.0f;
+                    if constexpr (Z) {
+                        const int byte = G == 128 ? 2 * (unit & 1) + gr : gr & 3;
+                        zero = 16.0f + (float)((zw[r][G == 32 ? gr / 4 : 0] >> (8 * byte)) & 15u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        sum[r][i] =
+                            __builtin_fmaf(scale, __builtin_fmaf(-zero, xs[i], acc[r][i]), sum[r][i]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    asm volatile("" : "+v"(sum[r][i]));     // see k_mv_i4
+        };
+
+        if (wave < p.units) {
+            const int last = p.units - 1;
+#pragma unroll
+            for (int d = 0; d < D - 1; ++d)
+                issue(min(wave + d * KW, last), d);
+            int slot = 0;
+            for (int unit = wave; unit < p.units; unit += KW) {
+                issue(min(unit + (D - 1) * KW, last), slot == 0 ? D - 1 : slot - 1);
+                // this unit has landed when only the D - 1 after it are outstanding
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kLoads) : "memory");
+                compute(unit, slot);
+                slot = slot == D - 1 ? 0 : slot + 1;
+            }
+        }
+        // this wave's ring holds its sums once the last loads have landed
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        float* red = reinterpret_cast<float*>(ring[wave]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                red[(r * NI + i) * 64 + lane] = sum[r][i];
+        __syncthreads();
+        for (int u = wave; u < R * NI; u += KW) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+                v += reinterpret_cast<const float*>(ring[w])[u * 64 + lane];
+            const int m = m0 + g + 4 * (u % NI), n = n0 + 16 * (u / NI) + n16;
+            if (m < p.rows && n < p.N)
+                p.y[m * p.ldy + n] = from_f32<F16>(v);
+        }
+        __syncthreads();
+    }
+}
+
+template <bool F16, int G, bool Z, bool Tail, int NI, int R, int KW, int D>
+hipError_t launch_ms(const Args& a0, hipStream_t st) {
+    Args a = a0;
+    const int64_t chunks = ((int64_t)a.rows + 4 * NI - 1) / (4 * NI);
+    a.chunk = (int32_t)(chunks < 16384 ? chunks : 16384);
+    const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), a.chunk);
+    return launch1(k_ms_i4<F16, G, Z, Tail, NI, R, KW, D>, grid, dim3(64 * KW), st, a);
+}
+
+// The kernel for few rows.  Rules and measurements on MI355X (us):
+//  - Dense, up to 16 rows: k_ms_i4, in chunks of 4, 8 or 16 rows, with 32 rows of W for each
+//    workgroup (1 x 7168 x 7168, group 128: 8.2), or 16 where 32 would leave half of the compute
+//    units without one (1 x 1024 x 43008: 18.0 against 31.7; 16 x 1024 x 43008 27.4 against 38).
+//    Its lanes' offsets have 32 bits; where rows are so far apart that they do not fit, k_mv_i4.
+//  - Above 16 rows k_mv_i4 with blocks of 16 tokens, two up to 32 rows (32 x 7168 x 7168: 19.9
+//    against 24.8 with four), else four.
+//  - By expert k_mv_i4 with four blocks of 16 rows of W to share the operands of x (8 rows for
+//    each of 64 experts of 4096 x 7168: 254 against 283 with two), or two where four leave
+//    less than two workgroups to a compute unit.
 template <bool F16, int G, bool Z, bool Tail>
 hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
     if (a.off) {
@@ -779,13 +997,20 @@ hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
             return launch_mv<F16, G, Z, Tail, 4, 1, 4, 4, 1>(a, st);
         return launch_mv<F16, G, Z, Tail, 4, 1, 2, 4, 1>(a, st);
     }
-    const bool narrow = a.N < 4096;
-    if (m <= 4)
-        return narrow ? launch_mv<F16, G, Z, Tail, 1, 1, 1, 8, 2>(a, st)
-                      : launch_mv<F16, G, Z, Tail, 1, 1, 2, 8, 1>(a, st);
-    if (m <= 16)
-        return narrow ? launch_mv<F16, G, Z, Tail, 4, 1, 1, 8, 1>(a, st)
-                      : launch_mv<F16, G, Z, Tail, 4, 1, 2, 8, 1>(a, st);
+    if (m <= 16) {
+        const bool narrow = a.N < 4096;
+        const auto near = [](int64_t rows, int64_t ld) { return ld < ((int64_t)1 << 31) / rows; };
+        if (!near(32, a.ldc) || !near(32, a.lds) || !near(32, a.ldz) || !near(16, a.ldx))
+            return launch_mv<F16, G, Z, Tail, 4, 1, 2, 4, 1>(a, st);
+        if (m <= 4)
+            return narrow ? launch_ms<F16, G, Z, Tail, 1, 1, 8, 3>(a, st)
+                          : launch_ms<F16, G, Z, Tail, 1, 2, 8, 2>(a, st);
+        if (m <= 8)
+            return narrow ? launch_ms<F16, G, Z, Tail, 2, 1, 8, 2>(a, st)
+                          : launch_ms<F16, G, Z, Tail, 2, 2, 4, 2>(a, st);
+        return narrow ? launch_ms<F16, G, Z, Tail, 4, 1, 4, 2>(a, st)
+                      : launch_ms<F16, G, Z, Tail, 4, 2, 4, 2>(a, st);
+    }
     if (m <= 32)
         return launch_mv<F16, G, Z, Tail, 4, 2, 2, 4, 1>(a, st);
     return launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);

@@ -55,10 +55,11 @@ bq_status bq_dequant_i4_f16(const uint8_t* c, int64_t ldc, const uint16_t* scale
                             int group, uint16_t* y, int64_t ldy, void* stream);
 
 /* Y[m][n] = bf16_rne( sum over k of X[m][k] * W[n][k] ): X bf16[M][ldx] (16-byte aligned,
- * ldx >= K, ldx % 8 == 0), W the I4 matrix of N rows; y bf16[M][ldy], ldy >= N.  For a group,
- * sum of x * (16 + code) and sum of x are accumulated in binary32 by the matrix cores (every
- * product is exact), and scale * (first - (16 + zero) * second) is added in binary32; y is
- * rounded once.  The order of the sums is fixed for given M, N, K.  M == 0 or N == 0
+ * ldx >= K, ldx % 8 == 0), W the I4 matrix of N rows; y bf16[M][ldy], ldy >= N.  The sums over
+ * a group are taken in binary32 by the matrix cores from exact products (of x and code -
+ * zero, or of x and 16 + code and of x alone, subtracted afterwards), the group's scale is
+ * applied to them in binary32, and y is rounded once.  The same call gives the same bits;
+ * the order of the sums depends on the sizes.  M == 0 or N == 0
  * launches nothing; K must be positive, M and K at most 2^30 and N at most 2^26 (else
  * BQ_ERR_SIZE).  y must not overlap an input.  _f16: X, scale and
  * Y are binary16. */
