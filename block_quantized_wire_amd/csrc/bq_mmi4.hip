@@ -10,9 +10,10 @@
 // at most a factor of 16 + zero over |code - zero| in the rounding of binary32 sums.  (bf16
 // has no packed subtraction; binary16 has, and k_mm_i4 subtracts the zero point there.)
 //
-// Three kernels, chosen by the row count (launch_shape): k_ms_i4 for up to 16 rows and k_mv_i4
-// for up to 192, bound by the bytes of the weights, and k_mm_i4, bound by the matrix cores
-// and the vector instructions that feed them.  Rates at a stated size stand at each.
+// Three kernels, chosen by the row counts (launch_shape): k_ms_i4 for up to 16 rows, bound by the
+// bytes of the weights; k_mv_i4 for more in products that keep few workgroups busy, bound by
+// the making of operands; and k_mm_i4, bound by the matrix cores and the vector
+// instructions that feed them.  Rates at a stated size stand at each.
 #include "bq_device.h"
 #include "bq_launch.h"
 
@@ -368,12 +369,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 
 // ---- many rows ------------------------------------------------------------------------------
 //
-// With many rows of x the matrix cores bound the work.  A workgroup of 4 waves computes TM rows
-// of x (128, or 64 where there are fewer) by 256 rows of W; a wave all TM by 64.  Stages
+// With many rows of x the matrix cores bound the work.  A workgroup computes TM rows of x (128,
+// or 64 where there are fewer) by 256 rows of W, each wave all TM by its share of them.  Stages
 // of 64 columns go through LDS, x and codes both, brought there by global-to-LDS loads in a
 // ring of three: while a stage is computed, the next one has landed or is landing and the one
 // after it is being fetched.  Scales and zero points come for several stages (a unit) at once.
-// Per stage a wave turns its 64 x 64 codes into operands once and uses them for all blocks of 16
+// Per stage a wave turns its codes into operands once and uses them for all blocks of 16
 // rows of x; each group's products start from zero and are multiplied by the scale into the
 // running sums, in registers.
 
@@ -389,10 +390,13 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // is read back behind the stage's loads (531 against 689 TFLOP/s), so the scales' addresses are
 // made anew and bf16 with zero points holds one block of x instead of two.
 constexpr int kTN = 256, kStage = 64;
-constexpr int kTileThreads = 256, kTileWaves = 4;
-constexpr int kWaveN = kTN / kTileWaves, kNB = kWaveN / 16;
+// Waves of a workgroup.  128-row tiles keep to 4, which read x from LDS half as often as 8 (32
+// experts as above, bf16: 929 us against 845); 64-row tiles gain from 8 where there are few
+// workgroups (256 x 7168 x 7168: 97 against 108) and lose nothing where there are many.
+template <int TM>
+constexpr int kTileWaves = TM == 128 ? 4 : 8;
 constexpr int kRing = 3;
-constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kMaxGridY = 65535, kComputeUnits = 256;
 
 template <int TM>
 struct alignas(16) TileStage {
@@ -489,10 +493,11 @@ __device__ __forceinline__ int find_block(const Args& p, int block, int& lo, int
 }
 
 template <bool F16, int G, bool Z, int TM>
-__global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
+__global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i4(Args p) {
     using Shared = TileShared<G, Z, F16, TM>;
     using Stage = TileStage<TM>;
-    constexpr int kMB = TM / 16, kXLoads = TM / 32;
+    constexpr int kWaves = kTileWaves<TM>, kWaveN = kTN / kWaves, kNB = kWaveN / 16, kMB = TM / 16;
+    constexpr int kXLoads = TM / (8 * kWaves), kWLoads = 8 / kWaves;
     __shared__ Shared sm;
     const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -508,50 +513,52 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
     const uint16_t* s = p.s + expert * p.stride_s;
     const uint8_t* z = Z ? p.z + expert * p.stride_z : nullptr;
 
-    // what this thread brings: x rows tid / 8 + 32 i, chunk tid % 8 (of the slot's row); codes of
-    // rows tid / 2 + 128 i, half tid % 2
+    // what this thread brings: x rows tid / 8 + 8 kWaves i, chunk tid % 8 (of the slot's row);
+    // codes of rows tid / 2 + 32 kWaves i, half tid % 2
     const uint16_t* xp[kXLoads];
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-        const int r = (tid >> 3) + 32 * i;
+        const int r = (tid >> 3) + 8 * kWaves * i;
         xp[i] = p.x + x_row(p, min(lo + r, hi - 1)) * p.ldx;
     }
     const int xc = 8 * ((tid & 7) ^ ((tid >> 3) & 7));
-    const uint8_t* cp[2];
+    const uint8_t* cp[kWLoads];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        cp[i] = c + min(n0 + (tid >> 1) + 128 * i, p.N - 1) * p.ldc;
+    for (int i = 0; i < kWLoads; ++i)
+        cp[i] = c + min(n0 + (tid >> 1) + 32 * kWaves * i, p.N - 1) * p.ldc;
     const int stages = (p.K + kStage - 1) / kStage;
     const auto issue = [&](int stage, int slot) {
         Stage& t = sm.stage[slot];
         const int k = stage * kStage;
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i)
-            lds_load16(xp[i] + min(k + xc, p.K - 8), t.x + wave * 1024 + i * 4096);
+            lds_load16(xp[i] + min(k + xc, p.K - 8), t.x + (wave + i * kWaves) * 1024);
         const int kc = min(k + 32 * (tid & 1), p.K - 32) / 2;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            lds_load16(cp[i] + kc, t.w + wave * 1024 + i * 4096);
+        for (int i = 0; i < kWLoads; ++i)
+            lds_load16(cp[i] + kc, t.w + (wave + i * kWaves) * 1024);
     };
-    // a wave's own 64 rows of scales and zero points, word by word
+    // a wave's own rows of scales and zero points, word by word
     constexpr int kS = Shared::kS, kUnitGroups = Shared::kUnit / G;
+    constexpr int kSLoads = (kWaveN * kS + 63) / 64;
     const int groups = p.K / G;
     const auto issue_scales = [&](int unit) {
         int l = lane;
         asm volatile("" : "+v"(l));     // addresses are made anew: registers are short
 #pragma unroll
-        for (int i = 0; i < kS; ++i) {
-            const int row = min(n0 + wave * kWaveN + i * (64 / kS) + l / kS, p.N - 1);
-            const int at = min(unit * kUnitGroups + 2 * (l % kS), (groups - 1) & ~1);
-            lds_load4(s + row * p.lds + at, &sm.s[unit & 1][(wave * kWaveN + i * (64 / kS)) * kS]);
-        }
-        if constexpr (Z) {
+        for (int i = 0; i < kSLoads; ++i)
+            if (kWaveN * kS % 64 == 0 || 64 * i + l < kWaveN * kS) {
+                const int row = min(n0 + wave * kWaveN + i * (64 / kS) + l / kS, p.N - 1);
+                const int at = min(unit * kUnitGroups + 2 * (l % kS), (groups - 1) & ~1);
+                lds_load4(s + row * p.lds + at, &sm.s[unit & 1][(wave * kWaveN + i * (64 / kS)) * kS]);
+            }
+        if (Z && (kWaveN == 64 || l < kWaveN)) {
             const int row = min(n0 + wave * kWaveN + l, p.N - 1);
             const int at = min(unit * kUnitGroups, groups - 1) & ~3;
             lds_load4(z + row * p.ldz + at, &sm.z[unit & 1][wave * kWaveN]);
         }
     };
-    constexpr int kStageLoads = kXLoads + 2, kScaleLoads = kS + (Z ? 1 : 0);
+    constexpr int kStageLoads = kXLoads + kWLoads, kScaleLoads = kSLoads + (Z ? 1 : 0);
 
     f32x4 sum[kMB][kNB];
 #pragma unroll
@@ -575,7 +582,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
     // (negative, and times the 24 of the constant zero point, where the products start from them)
     const auto sums_of_x = [&](const Stage& t) {
         const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-        for (int block = wave; block < kMB; block += kTileWaves) {
+        for (int block = wave; block < kMB; block += kWaves) {
             f32x4 a = mma<F16>(x_at(t, block, 0), ones, f32x4{});
             f32x4 b = mma<F16>(x_at(t, block, 1), ones, kHalves == 2 ? f32x4{} : a);
             a *= Z ? -1.0f : -24.0f;
@@ -607,7 +614,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
             sums_of_x(t);
         // bf16 with zero points has no registers for two blocks (a spill would wait for the loads
         // of later stages): its next operand is read when the last one has been used
-        constexpr int kXBufs = !F16 && Z ? 1 : 2;
+        constexpr int kXBufs = !F16 && Z && TM == 128 ? 1 : 2;
         u32x4 x[kXBufs][2];
         x[0][0] = x_at(t, 0, 0);
         x[0][1] = x_at(t, 0, 1);
@@ -655,11 +662,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
         const auto fold = [&](int step, int part) {
             const int m = step / kHalves, h = step % kHalves;
 #pragma unroll
-            for (int e = part * 16 / kSlots; e < (part + 1) * 16 / kSlots; ++e) {
+            for (int e = part * 4 * kNB / kSlots; e < (part + 1) * 4 * kNB / kSlots; ++e) {
                 const int b = e / 4, i = e % 4;
                 float v = acc[step & 1][b][i];
                 if constexpr (!F16 && Z)
-                    v = __builtin_fmaf(zero[b][h], xs[0][i], v);
+                    v = __builtin_fmaf(zero[b][h], xs[step % kXBufs][i], v);
                 sum[m][b][i] = __builtin_fmaf(scale[b][h], v, sum[m][b][i]);
             }
         };
@@ -668,7 +675,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
                 xs[step % kXBufs] = *reinterpret_cast<const f32x4*>(sm.xs + (step % kHalves) * TM +
                                                                16 * (step / kHalves) + 4 * g);
         };
-        if constexpr (!F16 && !Z)
+        if constexpr (kXBufs == 2)
             read_xs(0);
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
@@ -687,16 +694,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_mm_i4(Args p) {
                         x[(m + 1) & 1][0] = x_at(t, m + 1, 0);
                         x[(m + 1) & 1][1] = x_at(t, m + 1, 1);
                     }
-                    if (i == kSlots - 1 && step + 1 < kSteps)
-                        read_xs(step + 1);     // over those of the step before
                 } else {
                     if (b == kNB - 1 && m + 1 < kMB)
                         x[0][j] = x_at(t, m + 1, j);
                 }
                 if (step > 0)
                     fold(step - 1, i);
-                if (kXBufs == 1 && i == kSlots - 1)
-                    read_xs(step);         // for the scaling of this step, in the next
+                // over those of the step before, whose last use this was; with one block of x for
+                // the scaling of this step, in the next
+                if (i == kSlots - 1 && kXBufs == 1)
+                    read_xs(step);
+                else if (i == kSlots - 1 && step + 1 < kSteps)
+                    read_xs(step + 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -765,7 +774,7 @@ hipError_t launch_tile(const Args& a0, hipStream_t st) {
         a.block0 = (int32_t)b;
         const int64_t n = blocks - b < kMaxGridY ? blocks - b : kMaxGridY;
         const dim3 grid((unsigned)((a.N + kTN - 1) / kTN), (unsigned)n);
-        e = launch1(k_mm_i4<F16, G, Z, TM>, grid, dim3(kTileThreads), st, a);
+        e = launch1(k_mm_i4<F16, G, Z, TM>, grid, dim3(64 * kTileWaves<TM>), st, a);
     }
     return e;
 }
@@ -986,7 +995,8 @@ hipError_t launch_ms(const Args& a0, hipStream_t st) {
 //    units without one (1 x 1024 x 43008: 18.0 against 31.7; 16 x 1024 x 43008 27.4 against 38).
 //    Its lanes' offsets have 32 bits; where rows are so far apart that they do not fit, k_mv_i4.
 //  - Above 16 rows k_mv_i4 with blocks of 16 tokens, two up to 32 rows (32 x 7168 x 7168: 19.9
-//    against 24.8 with four), else four.
+//    against 24.8 with four), else four; 16 rows of W to a workgroup of 8 waves instead of 32 to 4
+//    where that still fits one round (64 x 1024 x 8192: 33 against 38, 24 rows 17 against 20).
 //  - By expert k_mv_i4 with four blocks of 16 rows of W to share the operands of x (8 rows for
 //    each of 64 experts of 4096 x 7168: 254 against 283 with two), or two where four leave
 //    less than two workgroups to a compute unit.
@@ -1011,21 +1021,27 @@ hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
         return narrow ? launch_ms<F16, G, Z, Tail, 4, 1, 4, 2>(a, st)
                       : launch_ms<F16, G, Z, Tail, 4, 2, 4, 2>(a, st);
     }
-    if (m <= 32)
-        return launch_mv<F16, G, Z, Tail, 4, 2, 2, 4, 1>(a, st);
-    return launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);
+    if (((int64_t)a.N + 15) / 16 * ((m + 63) / 64) <= kComputeUnits)
+        return m <= 32 ? launch_mv<F16, G, Z, Tail, 4, 2, 1, 8, 1>(a, st)
+                       : launch_mv<F16, G, Z, Tail, 4, 4, 1, 8, 1>(a, st);
+    return m <= 32 ? launch_mv<F16, G, Z, Tail, 4, 2, 2, 4, 1>(a, st)
+                   : launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);
 }
 
-// Few rows or many (us, bf16, group 128, 7168 x 7168): 192 rows 97 with the kernel for few
-// against 107 with the one for many, 256 rows 128 against 108.  By expert the kernel for many
-// wins from 16 rows an expert (64 experts of 4096 x 7168: 349 against 350 there, 403 against
-// 837 at 32).  Tiles of 128 rows where they make workgroups enough: 2048 rows 248 against
-// 297 with tiles of 64, 1024 rows 171 against 161; by expert 96 rows 684 against 668, 160 rows
-// 964 against 986.
+// Few rows or many.  k_mv_i4 runs in rounds of a workgroup per compute unit, k_mm_i4 for up to
+// two workgroups to each in the time of one (64-row tiles, 8192 columns: 108 us in bf16 with group
+// 128).  A workgroup of k_mv_i4 takes 64 rows of x by 32 rows of W, so three rounds of it are as
+// long (128 x 12288: 106 against 109; 128 x 14336: 138 against 110; 3000 x 512: 107 against 108;
+// 1000 x 1024: 73 against 107), and six of its form for up to 32 rows (24 x 40960: 93
+// against 110; 24 x 57344: 126 against 115).  By expert the kernel for many wins from 16 rows an
+// expert (64 experts of 4096 x 7168: 351 against 351 there, 407 against 837 at 32).  Tiles of 128
+// rows where they make workgroups enough (7168 x 7168): 2048 rows 251 against 297 with tiles of
+// 64, 1024 rows 171 against 156; by expert 96 rows 680 against 663, 160 rows 961 against 981.
 template <bool F16, int G, bool Z>
 hipError_t launch_shape(const Args& a, hipStream_t st) {
     const int64_t m = a.off ? (a.rows + a.experts - 1) / a.experts : a.rows;
-    if (m > (a.off ? 16 : 192)) {
+    const int64_t few = ((int64_t)a.N + 31) / 32 * ((m + 63) / 64);
+    if (m > 16 && (a.off || few > (m <= 32 ? 6 : 3) * kComputeUnits)) {
         const int64_t tiles = (m + 127) / 128 * ((a.N + kTN - 1) / kTN);
         const bool tall = a.off ? m > 128 : tiles >= 384;
         return tall ? launch_tile<F16, G, Z, 128>(a, st) : launch_tile<F16, G, Z, 64>(a, st);

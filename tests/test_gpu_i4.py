@@ -86,6 +86,16 @@ def test_many_rows(m, n, k, group, kind):
     check_mm(m, n, k, group, kind, False, pad=True)
 
 
+@pytest.mark.parametrize("m,n", [(4100, 401), (24583, 300), (65, 12300), (20, 49170), (3000, 70),
+                                 (20, 4000)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_many_workgroups(m, n, group, kind):
+    """Long on one side, with depths that end inside a stage or a unit of scales."""
+    check_mm(m, n, {32: 160, 64: 192, 128: 384}[group], group, kind, True, exact=True)
+    check_mm(m, n, {32: 32, 64: 320, 128: 128}[group], group, kind, False, exact=True, pad=True)
+
+
 def test_extremes_of_codes_and_zero_points():
     """Codes 0 and 15 against zero points 0 and 15, scales of 0 and of the type's largest and
     smallest normal numbers, rows of x that are all zero."""
