@@ -369,52 +369,65 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 
 // ---- many rows ------------------------------------------------------------------------------
 //
-// With many rows of x the matrix cores bound the work.  A workgroup computes TM rows of x (128,
-// or 64 where there are fewer) by 256 rows of W, each wave all TM by its share of them.  Stages
-// of 64 columns go through LDS, x and codes both, brought there by global-to-LDS loads in a
-// ring of three: while a stage is computed, the next one has landed or is landing and the one
-// after it is being fetched.  Scales and zero points come for several stages (a unit) at once.
+// With many rows of x the matrix cores bound the work.  A workgroup computes TM x TN results (TM
+// rows of x, TN rows of W), each wave all TM rows by its share of the others.  Stages of 64 columns
+// go through LDS, x and codes both, brought there by global-to-LDS loads in a ring of three: while
+// a stage is computed, the next one has landed or is landing and the one after it is being
+// fetched.  Scales and zero points come for several stages (a unit) at once.
 // Per stage a wave turns its codes into operands once and uses them for all blocks of 16
 // rows of x; each group's products start from zero and are multiplied by the scale into the
 // running sums, in registers.
-
-// Measured on MI355X (a large library product reaches 1400 TFLOP/s): 24594 sorted rows over 32
-// experts of 2048 x 7168, group 64 with zero points, 845 us in binary16 (854 TFLOP/s) and 1048
-// in bf16, whose zero points cost a second multiply-add for each result; group 128 without
-// 773 (934 TFLOP/s) and 917.  What bounds it are the instructions between the matrix
-// instructions: 264 vector and 64 matrix instructions a stage and wave, of which 128 scale
-// results and 88 make operands, with two waves to a SIMD.  Scaling the operands instead of the
-// results would save half of them and round every weight to 8 (11) bits, which it must not.
-// bf16's sums of x are made inside the stage, with a barrier of their own: made a stage ahead
-// they need a stage more in flight (1146 against 917 us).  Registers are short: a spilled one
-// is read back behind the stage's loads (531 against 689 TFLOP/s), so the scales' addresses are
-// made anew and bf16 with zero points holds one block of x instead of two.
-constexpr int kTN = 256, kStage = 64;
-// Waves of a workgroup.  128-row tiles keep to 4, which read x from LDS half as often as 8 (32
-// experts as above, bf16: 929 us against 845); 64-row tiles gain from 8 where there are few
-// workgroups (256 x 7168 x 7168: 97 against 108) and lose nothing where there are many.
-template <int TM>
-constexpr int kTileWaves = TM == 128 ? 4 : 8;
-constexpr int kRing = 3;
+//
+// 128 x 256, 4 waves, two workgroups to a compute unit.  Measured on MI355X (a large library
+// product reaches 1400 TFLOP/s): 24594 sorted rows over 32 experts of 2048 x 7168, group 64 with
+// zero points, 846 to 860 us in binary16 (840 to 854 TFLOP/s) and 1048 in bf16, whose zero points
+// cost a second multiply-add for each result; group 128 without 773 (934 TFLOP/s) and 917.
+// What bounds it are the instructions between the matrix instructions: 264 vector and 64 matrix
+// instructions a stage and wave, of which 128 scale results and 88 make operands, with two
+// waves to a SIMD.  Scaling the operands instead of the results would save half of them and
+// round every weight to 8 (11) bits, which it must not.  bf16's sums of x are made inside the
+// stage, with a barrier of their own: made a stage ahead they need a stage more in flight
+// (1146 against 917 us).  Registers are short: a spilled one is read back behind the stage's
+// loads (531 against 689 TFLOP/s), so the scales' addresses are made anew and bf16 with zero
+// points holds one block of x instead of two.  8 waves read x from LDS twice as often (929
+// against 845 us).
+//
+// 64 x 256, 8 waves: fewer rows an expert, or fewer workgroups (256 x 7168 x 7168: 97 us, and
+// 108 with 4 waves).
+//
+// 64 x 128, 4 waves in each of two parts, for products that leave compute units idle.  There a
+// stage's chain (LDS to registers, sums of x, a barrier, operands, products) takes the time, 0.8 us
+// whatever else runs.  So a stage's inputs are read from LDS a stage ahead, each wave makes the sums
+// of x for itself (8 matrix instructions more on 16), the ring holds six stages, and the
+// two parts of a workgroup take half of the columns each and add their sums at the end.
+// 256 x 7168 x 7168: 97 us as 64 x 256, 84 as 64 x 128, 68 with inputs a stage ahead, 55 in two
+// parts (19 at the rate of a large product).
+constexpr int kStage = 64;
+// Waves of a part of a workgroup, and its parts.
+template <int TM, int TN>
+constexpr int kTileWaves = TM == 128 ? 4 : TN / 32;
+template <int TN>
+constexpr int kTileParts = TN == 128 ? 2 : 1;
 constexpr int64_t kMaxGridY = 65535, kComputeUnits = 256;
 
-template <int TM>
+template <int TM, int TN>
 struct alignas(16) TileStage {
     uint8_t x[TM * 128];     // rows of 8 chunks of 16 bytes; chunk c of row r in slot c ^ (r & 7)
-    uint8_t w[kTN * 32];     // rows of 32 bytes of codes
+    uint8_t w[TN * 32];     // rows of 32 bytes of codes
 };
 
-template <int G, bool Z, bool F16, int TM>
+template <int G, bool Z, bool F16, int TM, int TN>
 struct alignas(16) TileShared {
     static constexpr int kUnit = G == 32 ? 128 : 256;    // columns whose scales come together
     static constexpr int kS = kUnit / G / 2;             // words of scales of a row and unit
-    TileStage<TM> stage[kRing];
-    uint32_t s[2][kTN * kS];
-    uint32_t z[Z ? 2 : 1][Z ? kTN : 1];                  // one word of zero points
+    static constexpr int kRing = TN == 128 ? 6 : 3;
+    TileStage<TM, TN> stage[kRing];
+    uint32_t s[2][TN * kS];
+    uint32_t z[Z ? 2 : 1][Z ? TN : 1];                   // one word of zero points
     alignas(16) float xs[F16 ? 4 : 2 * TM];              // sums of x per row and half stage
 };
 // two workgroups of 128 rows fit a compute unit's 160 KB
-static_assert(sizeof(TileShared<32, true, false, 128>) <= 80 * 1024, "LDS of a workgroup");
+static_assert(sizeof(TileShared<32, true, false, 128, 256>) <= 80 * 1024, "LDS of a workgroup");
 
 // The 8 codes of a word as operands in column order, less the zero point where the type has
 // a packed subtraction.  Codes 2i, 2i+1 are byte i of the even and of the odd nibbles.
@@ -492,15 +505,20 @@ __device__ __forceinline__ int find_block(const Args& p, int block, int& lo, int
     return -1;
 }
 
-template <bool F16, int G, bool Z, int TM>
-__global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i4(Args p) {
-    using Shared = TileShared<G, Z, F16, TM>;
-    using Stage = TileStage<TM>;
-    constexpr int kWaves = kTileWaves<TM>, kWaveN = kTN / kWaves, kNB = kWaveN / 16, kMB = TM / 16;
-    constexpr int kXLoads = TM / (8 * kWaves), kWLoads = 8 / kWaves;
-    __shared__ Shared sm;
-    const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g = lane >> 4;
+template <bool F16, int G, bool Z, int TM, int TN>
+__global__ __launch_bounds__((64 * kTileWaves<TM, TN> * kTileParts<TN>), TM == 128 || TN == 128 ? 2 : 4) void k_mm_i4(Args p) {
+    using Shared = TileShared<G, Z, F16, TM, TN>;
+    using Stage = TileStage<TM, TN>;
+    constexpr int kRing = Shared::kRing;
+    constexpr int kWaves = kTileWaves<TM, TN>, kWaveN = TN / kWaves, kNB = kWaveN / 16, kMB = TM / 16;
+    constexpr int kXLoads = TM / (8 * kWaves), kWLoads = TN / (32 * kWaves);
+    __shared__ Shared parts[kTileParts<TN>];
+    constexpr bool kOne = kTileParts<TN> == 1;
+    const int tid = kOne ? threadIdx.x : threadIdx.x & (64 * kWaves - 1);
+    const int lane = tid & 63, n16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int part = kOne ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kWaves));
+    Shared& sm = parts[part];
     int lo, hi;
     const int expert =
         __builtin_amdgcn_readfirstlane(find_block<TM>(p, p.block0 + blockIdx.y, lo, hi));
@@ -508,7 +526,7 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
         return;
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(min(hi, lo + TM));
-    const int n0 = blockIdx.x * kTN;
+    const int n0 = blockIdx.x * TN;
     const uint8_t* c = p.c + expert * p.stride_c;
     const uint16_t* s = p.s + expert * p.stride_s;
     const uint8_t* z = Z ? p.z + expert * p.stride_z : nullptr;
@@ -596,20 +614,65 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
             }
         }
     };
-    const auto compute = [&](int stage, int q, int slot, int unit) {
-        const Stage& t = sm.stage[slot];
-        // everything the operands are made of is read first, and block 0 of x
-        u32x2 raw[kNB];
-        uint32_t sw[kNB], zw[kNB];
+    // What a stage's operands are made of, and the operands with their scales and zero points.
+    struct Raw {
+        u32x2 c[kNB];
+        uint32_t s[kNB], z[kNB];
+    };
+    struct Operands {
+        u32x4 w[kNB][2];
+        float scale[kNB][kHalves], zero[kNB][kHalves];
+    };
+    const auto read_raw = [&](Raw& raw, int q, int slot, int unit) {
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
             const int row = wave * kWaveN + 16 * b + n16;
-            raw[b] = *reinterpret_cast<const u32x2*>(t.w + row * 32 + 8 * g);
+            raw.c[b] = *reinterpret_cast<const u32x2*>(sm.stage[slot].w + row * 32 + 8 * g);
             // the word with this stage's group (or its two)
-            sw[b] = sm.s[unit & 1][row * kS + (G == 128 ? 0 : G == 64 ? q / 2 : q)];
+            raw.s[b] = sm.s[unit & 1][row * kS + (G == 128 ? 0 : G == 64 ? q / 2 : q)];
             if constexpr (Z)
-                zw[b] = sm.z[unit & 1][row];
+                raw.z[b] = sm.z[unit & 1][row];
         }
+    };
+    const auto make = [&](Operands& o, Raw& raw, int stage, int q, int unit) {
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+            if constexpr (G == 32) {
+                const auto v =
+                    __builtin_amdgcn_permlane32_swap(raw.c[b].x, raw.c[b].y, false, false);
+                raw.c[b] = u32x2{v[0], v[1]};
+            }
+            h16x2 less[kHalves];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                const int half = G == 128 ? q / 2 : G == 64 ? q & 1 : h;    // of the word
+                float scale = to_f32<F16>(raw.s[b] >> (16 * half)), zero = 8.0f;
+                if (h == 1 && stage * kStage + 32 >= p.K)   // half a last stage
+                    scale = 0.0f;
+                if constexpr (Z) {
+                    const int byte = G == 128 ? 2 * (unit & 1) + q / 2 : G == 64 ? q : 2 * q + h;
+                    zero = (float)((raw.z[b] >> (8 * byte)) & 15u);
+                }
+                if constexpr (F16) {
+                    scale *= 512.0f;
+                    const _Float16 l = (_Float16)(zero * (-1.0f / 512.0f));
+                    less[h] = h16x2{l, l};
+                } else {
+                    less[h] = h16x2{};
+                    zero += 16.0f;
+                }
+                o.scale[b][h] = scale;
+                o.zero[b][h] = zero;
+            }
+            o.w[b][0] = codes.operands(raw.c[b].x, less[0]);
+            o.w[b][1] = codes.operands(raw.c[b].y, less[kHalves - 1]);
+        }
+    };
+    const auto compute = [&](int stage, int q, int slot, int unit) {
+        const Stage& t = sm.stage[slot];
+        // everything the operands are made of is read first, and block 0 of x
+        Raw raw;
+        read_raw(raw, q, slot, unit);
         if constexpr (!F16)
             sums_of_x(t);
         // bf16 with zero points has no registers for two blocks (a spill would wait for the loads
@@ -618,38 +681,8 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
         u32x4 x[kXBufs][2];
         x[0][0] = x_at(t, 0, 0);
         x[0][1] = x_at(t, 0, 1);
-        u32x4 w[kNB][2];
-        float scale[kNB][kHalves], zero[kNB][kHalves];
-#pragma unroll
-        for (int b = 0; b < kNB; ++b) {
-            if constexpr (G == 32) {
-                const auto v = __builtin_amdgcn_permlane32_swap(raw[b].x, raw[b].y, false, false);
-                raw[b] = u32x2{v[0], v[1]};
-            }
-            h16x2 less[kHalves];
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                const int half = G == 128 ? q / 2 : G == 64 ? q & 1 : h;    // of the word
-                scale[b][h] = to_f32<F16>(sw[b] >> (16 * half));
-                if (h == 1 && stage * kStage + 32 >= p.K)   // half a last stage
-                    scale[b][h] = 0.0f;
-                zero[b][h] = 8.0f;
-                if constexpr (Z) {
-                    const int byte = G == 128 ? 2 * (unit & 1) + q / 2 : G == 64 ? q : 2 * q + h;
-                    zero[b][h] = (float)((zw[b] >> (8 * byte)) & 15u);
-                }
-                if constexpr (F16) {
-                    scale[b][h] *= 512.0f;
-                    const _Float16 l = (_Float16)(zero[b][h] * (-1.0f / 512.0f));
-                    less[h] = h16x2{l, l};
-                } else {
-                    less[h] = h16x2{};
-                    zero[b][h] += 16.0f;
-                }
-            }
-            w[b][0] = codes.operands(raw[b].x, less[0]);
-            w[b][1] = codes.operands(raw[b].y, less[kHalves - 1]);
-        }
+        Operands o;
+        make(o, raw, stage, q, unit);
         if constexpr (!F16)     // the other waves' sums of x
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
@@ -666,8 +699,8 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
                 const int b = e / 4, i = e % 4;
                 float v = acc[step & 1][b][i];
                 if constexpr (!F16 && Z)
-                    v = __builtin_fmaf(zero[b][h], xs[step % kXBufs][i], v);
-                sum[m][b][i] = __builtin_fmaf(scale[b][h], v, sum[m][b][i]);
+                    v = __builtin_fmaf(o.zero[b][h], xs[step % kXBufs][i], v);
+                sum[m][b][i] = __builtin_fmaf(o.scale[b][h], v, sum[m][b][i]);
             }
         };
         const auto read_xs = [&](int step) {
@@ -688,7 +721,7 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
                     from = acc[step & 1][b];
                 else if (!F16 && !Z)
                     from = xs[step % kXBufs];
-                acc[step & 1][b] = mma<F16>(x[m % kXBufs][j], w[b][j], from);
+                acc[step & 1][b] = mma<F16>(x[m % kXBufs][j], o.w[b][j], from);
                 if constexpr (kXBufs == 2) {
                     if (i == 0 && h == 0 && m + 1 < kMB) {
                         x[(m + 1) & 1][0] = x_at(t, m + 1, 0);
@@ -720,28 +753,144 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
                 asm volatile("" : "+v"(sum[m][b]));
     };
 
-    issue_scales(0);
-    issue(0, 0);
-    issue(min(1, stages - 1), 1);
-    wait_and_join<0>();
-    int slot = 0;
     constexpr int kUnitStages = Shared::kUnit / kStage;
-    for (int unit = 0; unit * kUnitStages < stages; ++unit) {
+    if constexpr (TN == 128) {
+        // A stage's inputs, read from LDS during the stage before it; a wave makes the sums of x
+        // for itself, so the waves meet once a stage.
+        struct Inputs {
+            Raw raw;
+            u32x4 x[kMB][2];
+        };
+        const auto read = [&](Inputs& in, int q, int slot, int unit) {
+            read_raw(in.raw, q, slot, unit);
 #pragma unroll
-        for (int q = 0; q < kUnitStages; ++q) {
-            const int stage = unit * kUnitStages + q;
-            const int next = slot == kRing - 1 ? 0 : slot + 1;
-            issue(min(stage + 2, stages - 1), next == kRing - 1 ? 0 : next + 1);
-            if (q == 0)
-                issue_scales(unit + 1);
-            if (stage < stages)
-                compute(stage, q, slot, unit);
-            // the next stage has landed when only what this one issued is outstanding
-            if (q == 0)
-                wait_and_join<kStageLoads + kScaleLoads>();
-            else
-                wait_and_join<kStageLoads>();
-            slot = next;
+            for (int m = 0; m < kMB; ++m) {
+                in.x[m][0] = x_at(sm.stage[slot], m, 0);
+                in.x[m][1] = x_at(sm.stage[slot], m, 1);
+            }
+        };
+        const auto compute_read = [&](Inputs& in, int stage, int q, int unit) {
+            Operands o;
+            make(o, in.raw, stage, q, unit);
+            const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            f32x4 xs[kMB][kHalves], acc[kMB][kNB][kHalves];
+#pragma unroll
+            for (int m = 0; m < kMB; ++m)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    xs[m][h] = f32x4{};
+                    if constexpr (!F16) {
+                        xs[m][h] = mma<F16>(in.x[m][h], ones, f32x4{});
+                        if (kHalves == 1)
+                            xs[m][h] = mma<F16>(in.x[m][1], ones, xs[m][h]);
+                        xs[m][h] *= Z ? -1.0f : -24.0f;
+                    }
+                }
+#pragma unroll
+            for (int m = 0; m < kMB; ++m)
+#pragma unroll
+                for (int b = 0; b < kNB; ++b)
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        f32x4 from{};
+                        if (!F16 && !Z)
+                            from = xs[m][h];
+                        acc[m][b][h] = mma<F16>(in.x[m][h], o.w[b][h], from);
+                        if (kHalves == 1)
+                            acc[m][b][h] = mma<F16>(in.x[m][1], o.w[b][1], acc[m][b][h]);
+                    }
+#pragma unroll
+            for (int m = 0; m < kMB; ++m)
+#pragma unroll
+                for (int b = 0; b < kNB; ++b) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v = acc[m][b][h][i];
+                            if constexpr (!F16 && Z)
+                                v = __builtin_fmaf(o.zero[b][h], xs[m][h][i], v);
+                            sum[m][b][i] = __builtin_fmaf(o.scale[b][h], v, sum[m][b][i]);
+                        }
+                    asm volatile("" : "+v"(sum[m][b]));     // (see k_mv_i4)
+                }
+        };
+        // each part takes its units of the columns; what is past them is fetched and not used
+        const int units = (stages + kUnitStages - 1) / kUnitStages, share = (units + 1) / 2;
+        const int first = part * share;
+        const auto fetch = [&](int stage, int slot) { issue(min(stage, stages - 1), slot); };
+        issue_scales(first);
+#pragma unroll
+        for (int d = 0; d < kRing - 1; ++d)
+            fetch(first * kUnitStages + d, d);
+        wait_and_join<0>();
+        Inputs in[2];
+        read(in[0], 0, 0, first);
+        int slot = 0;
+        for (int unit = first; unit < first + share; ++unit) {
+#pragma unroll
+            for (int q = 0; q < kUnitStages; ++q) {
+                constexpr int kLast = kUnitStages - 1;
+                const int stage = unit * kUnitStages + q, next = slot == kRing - 1 ? 0 : slot + 1;
+                if (q == 0)
+                    issue_scales(unit + 1);
+                // into the slot that was read two stages ago
+                fetch(stage + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);
+                read(in[(q + 1) & 1], q == kLast ? 0 : q + 1, next, q == kLast ? unit + 1 : unit);
+                __builtin_amdgcn_sched_barrier(0);
+                if (stage < stages)
+                    compute_read(in[q & 1], stage, q, unit);
+                // the stage after the next has landed, and before the unit's last stage the next
+                // unit's scales, which kLast stages were asked for after
+                if (q == kLast - 1)
+                    wait_and_join<(kLast < kRing - 3 ? kLast : kRing - 3) * kStageLoads>();
+                else
+                    wait_and_join<(kRing - 3) * kStageLoads>();
+                slot = next;
+            }
+        }
+        // the second part's sums to the first, through LDS that nothing lands in any more
+        wait_and_join<0>();
+        f32x4* trade = reinterpret_cast<f32x4*>(&parts[0]) + wave * kMB * kNB * 64 + lane;
+        static_assert(sizeof(Shared) >= TM * TN * sizeof(float), "room for the sums");
+        if (part == 1) {
+#pragma unroll
+            for (int m = 0; m < kMB; ++m)
+#pragma unroll
+                for (int b = 0; b < kNB; ++b)
+                    trade[(m * kNB + b) * 64] = sum[m][b];
+        }
+        wait_and_join<0>();
+        if (part == 1)
+            return;
+#pragma unroll
+        for (int m = 0; m < kMB; ++m)
+#pragma unroll
+            for (int b = 0; b < kNB; ++b)
+                sum[m][b] += trade[(m * kNB + b) * 64];
+    } else {
+        issue_scales(0);
+        issue(0, 0);
+        issue(min(1, stages - 1), 1);
+        wait_and_join<0>();
+        int slot = 0;
+        for (int unit = 0; unit * kUnitStages < stages; ++unit) {
+#pragma unroll
+            for (int q = 0; q < kUnitStages; ++q) {
+                const int stage = unit * kUnitStages + q;
+                const int next = slot == kRing - 1 ? 0 : slot + 1;
+                issue(min(stage + 2, stages - 1), next == kRing - 1 ? 0 : next + 1);
+                if (q == 0)
+                    issue_scales(unit + 1);
+                if (stage < stages)
+                    compute(stage, q, slot, unit);
+                // the next stage has landed when only what this one issued is outstanding
+                if (q == 0)
+                    wait_and_join<kStageLoads + kScaleLoads>();
+                else
+                    wait_and_join<kStageLoads>();
+                slot = next;
+            }
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands in LDS after the end
@@ -764,7 +913,7 @@ __global__ __launch_bounds__(64 * kTileWaves<TM>, TM == 128 ? 2 : 4) void k_mm_i
     }
 }
 
-template <bool F16, int G, bool Z, int TM>
+template <bool F16, int G, bool Z, int TM, int TN>
 hipError_t launch_tile(const Args& a0, hipStream_t st) {
     Args a = a0;
     // experts: every expert's last block may be partial
@@ -773,8 +922,8 @@ hipError_t launch_tile(const Args& a0, hipStream_t st) {
     for (int64_t b = 0; b < blocks && e == hipSuccess; b += kMaxGridY) {
         a.block0 = (int32_t)b;
         const int64_t n = blocks - b < kMaxGridY ? blocks - b : kMaxGridY;
-        const dim3 grid((unsigned)((a.N + kTN - 1) / kTN), (unsigned)n);
-        e = launch1(k_mm_i4<F16, G, Z, TM>, grid, dim3(64 * kTileWaves<TM>), st, a);
+        const dim3 grid((unsigned)((a.N + TN - 1) / TN), (unsigned)n);
+        e = launch1(k_mm_i4<F16, G, Z, TM, TN>, grid, dim3(64 * kTileWaves<TM, TN> * kTileParts<TN>), st, a);
     }
     return e;
 }
@@ -1028,26 +1177,32 @@ hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
                    : launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);
 }
 
-// Few rows or many.  k_mv_i4 runs in rounds of a workgroup per compute unit, k_mm_i4 for up to
-// two workgroups to each in the time of one (64-row tiles, 8192 columns: 108 us in bf16 with group
-// 128).  A workgroup of k_mv_i4 takes 64 rows of x by 32 rows of W, so three rounds of it are as
-// long (128 x 12288: 106 against 109; 128 x 14336: 138 against 110; 3000 x 512: 107 against 108;
-// 1000 x 1024: 73 against 107), and six of its form for up to 32 rows (24 x 40960: 93
-// against 110; 24 x 57344: 126 against 115).  By expert the kernel for many wins from 16 rows an
-// expert (64 experts of 4096 x 7168: 351 against 351 there, 407 against 837 at 32).  Tiles of 128
-// rows where they make workgroups enough (7168 x 7168): 2048 rows 251 against 297 with tiles of
-// 64, 1024 rows 171 against 156; by expert 96 rows 680 against 663, 160 rows 961 against 981.
+// The kernel and tile for many rows (us, bf16, group 128, 8192 columns where no others are given):
+//  - k_mv_i4 while its workgroups, 64 rows of x by 32 of W, fit one round of a workgroup per
+//    compute unit: 64 x 8192 41 against 58 in tiles of 64 x 128, 64 x 16384 74 against 59.  Up to 32
+//    rows its rounds are shorter and three are taken (24 x 24576: 62 against 62), or six where such
+//    tiles would not fit one round (24 x 40960: 93 against 110; 24 x 57344: 126 against 115).
+//  - Tiles of 64 x 128, in two parts of the columns, while they fit one round: 256 x 7168 x 7168
+//    55 against 97 in tiles of 64 x 256; 512 x 7168 x 7168, 448 of them, 108 against 98.
+//  - Tiles of 128 x 256 where they make workgroups enough (7168 x 7168): 2048 rows 251 against
+//    297 in tiles of 64, 1024 rows 171 against 156; by expert 96 rows 680 against 663, 160 rows
+//    961 against 981.
+//  - By expert the tiles win from 16 rows an expert (64 experts of 4096 x 7168: 351 against 351
+//    there, 407 against 837 at 32).
 template <bool F16, int G, bool Z>
 hipError_t launch_shape(const Args& a, hipStream_t st) {
     const int64_t m = a.off ? (a.rows + a.experts - 1) / a.experts : a.rows;
-    const int64_t few = ((int64_t)a.N + 31) / 32 * ((m + 63) / 64);
-    if (m > 16 && (a.off || few > (m <= 32 ? 6 : 3) * kComputeUnits)) {
-        const int64_t tiles = (m + 127) / 128 * ((a.N + kTN - 1) / kTN);
-        const bool tall = a.off ? m > 128 : tiles >= 384;
-        return tall ? launch_tile<F16, G, Z, 128>(a, st) : launch_tile<F16, G, Z, 64>(a, st);
-    }
-    return a.K % kUnit != 0 ? launch_few<F16, G, Z, true>(a, m, st)
-                            : launch_few<F16, G, Z, false>(a, m, st);
+    // of 64 rows of x; experts: every expert's last one may be partial
+    const int64_t blocks = a.off ? a.rows / 64 + a.experts : (m + 63) / 64;
+    const bool one_round = blocks * ((a.N + 127) / 128) <= kComputeUnits;
+    const int rounds = m > 32 ? 1 : one_round ? 3 : 6;
+    if (m <= 16 || (!a.off && blocks * ((a.N + 31) / 32) <= rounds * kComputeUnits))
+        return a.K % kUnit != 0 ? launch_few<F16, G, Z, true>(a, m, st)
+                                : launch_few<F16, G, Z, false>(a, m, st);
+    if (one_round)
+        return launch_tile<F16, G, Z, 64, 128>(a, st);
+    const bool tall = a.off ? m > 128 : (m + 127) / 128 * ((a.N + 255) / 256) >= 384;
+    return tall ? launch_tile<F16, G, Z, 128, 256>(a, st) : launch_tile<F16, G, Z, 64, 256>(a, st);
 }
 
 template <bool F16, int G>

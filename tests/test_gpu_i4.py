@@ -96,6 +96,24 @@ def test_many_workgroups(m, n, group, kind):
     check_mm(m, n, {32: 32, 64: 320, 128: 128}[group], group, kind, False, exact=True, pad=True)
 
 
+@pytest.mark.parametrize("m,n", [(1100, 700), (333, 2000), (40, 10001)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_rows_for_one_round_of_workgroups(m, n, group, kind):
+    """Two parts of the columns: one or none for the second, an odd unit, ends inside one."""
+    for cols in (128, 256, 384, 640, 1152):
+        check_mm(m, n, cols, group, kind, cols != 640, exact=True, pad=cols == 384)
+    check_mm(m, n, {32: 1056, 64: 1088, 128: 2176}[group], group, kind, True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("each,n", [([21, 0, 17, 40] * 15, 600), ([201, 0, 260, 129] * 10, 900)])
+def test_many_rows_by_expert(each, n, group, kind):
+    check_experts(each, n, 384, group, kind, True, False)
+    check_experts(each, n, 128, group, kind, False, True)
+
+
 def test_extremes_of_codes_and_zero_points():
     """Codes 0 and 15 against zero points 0 and 15, scales of 0 and of the type's largest and
     smallest normal numbers, rows of x that are all zero."""
