@@ -190,6 +190,24 @@ def test_weights_past_32_bit_offsets():
         assert bool((y[:, : n - 2] == 0).all())
 
 
+@pytest.mark.parametrize("m,n", [(4, 40), (16, 40), (17, 40), (17, 20000), (70, 6100)])
+def test_rows_of_x_far_apart(m, n):
+    """Rows of x more than 2^31 bytes apart in all, for every kernel."""
+    rng = np.random.default_rng([m, n])
+    k, ld = 640, 8 * ((1 << 28) // m + 1)
+    say(f"mm_i4 m={m} n={n} ldx={ld}")
+    codes, scale, zero = ref.matrix(rng, n, k, 64, "bf16", True, exact=True)
+    x = rows_of_x(rng, m, k, "bf16", True)
+    base = torch.empty((m - 1) * ld + k, dtype=torch.bfloat16, device=DEV)
+    far = base.as_strided((m, k), (ld, 1))
+    far.copy_(x)
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    bq.bq_mm_i4(far, dev(codes), dev(scale), y, zero=dev(zero), group=64)
+    sync()
+    want, _ = ref.product(x, codes, scale, zero, k, 64, "bf16")
+    assert torch.equal(y.cpu(), ref.rne(want, "bf16"))
+
+
 # ---- expert products -----------------------------------------------------------------------
 
 def check_experts(counts, n, k, group, kind, zeros, gathered, exact=True, tail=0, seed=0):
