@@ -1,12 +1,12 @@
-"""libblockq: block-quantized wire codecs for AMD MI355X (gfx950).
+"""libblockq: block-quantized wire codecs and an expert layer for AMD MI355X (gfx950).
 
 A thin ctypes binding over the C ABI declared in ``include/blockq.h`` and
-``include/blockq_moe.h``.  Every
-function here has the name of the C entry point it calls and only marshals
-arguments: torch tensors give device pointers, the stream defaults to torch's
-current stream, and a non-OK status raises :class:`BlockqError`.  All compute
-runs in the HIP kernels of ``libblockq.so``; there is no fallback, so importing
-fails loudly when the library has not been built.
+``include/blockq_moe.h``.  Every function here has the name of the C entry point
+it calls and only marshals arguments: torch tensors give device pointers, the
+stream defaults to torch's current stream, and a non-OK status raises
+:class:`BlockqError`.  All compute runs in the HIP kernels of ``libblockq.so``;
+there is no fallback, so importing fails loudly when the library has not been
+built.
 
 Tensor conventions: bf16 data as ``torch.bfloat16`` (or int16/uint16 bit
 views), INT8 payloads ``torch.int8``, E4M3 / E8M0 bytes ``torch.uint8``, block
