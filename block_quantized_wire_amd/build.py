@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libblockq.so")
 SOURCES = ["bq_abi.cpp", "bq_i8.hip", "bq_mx.hip", "bq_mxc.hip", "bq_mm.hip", "bq_noalloc.hip",
            "bq_i4.hip", "bq_mmi4.hip", "bq_moe.hip"]
-HEADERS = ["bq_device.h", "bq_launch.h"]
+HEADERS = ["bq_device.h", "bq_launch.h", "bq_ranges.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

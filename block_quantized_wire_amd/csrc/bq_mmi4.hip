@@ -16,6 +16,7 @@
 // instructions that feed them.  Rates at a stated size stand at each.
 #include "bq_device.h"
 #include "bq_launch.h"
+#include "bq_ranges.h"
 
 namespace bq {
 
@@ -201,8 +202,9 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
     int lo = blockIdx.y * kTokens, hi = p.rows, stride = p.chunk * kTokens;
     if (p.off) {
         const int e = blockIdx.y;
-        lo = max(p.off[e], 0);
-        hi = min(p.off[e + 1], p.rows);
+        const RowRange r = expert_rows(p.off[e], p.off[e + 1], p.rows);
+        lo = r.lo;
+        hi = r.hi;
         stride = kTokens;
         c += e * p.stride_c;
         s += e * p.stride_s;
@@ -481,12 +483,10 @@ __device__ __forceinline__ int find_block(const Args& p, int block, int& lo, int
     int seen = 0;
     for (int base = 0; base < p.experts; base += 64) {
         const int e = base + lane;
-        int first = 0, end = 0;
-        if (e < p.experts) {
-            first = max(p.off[e], 0);
-            end = min(p.off[e + 1], p.rows);
-        }
-        const int mine = max(end - first + TM - 1, 0) / TM;
+        RowRange r{0, 0};
+        if (e < p.experts)
+            r = expert_rows(p.off[e], p.off[e + 1], p.rows);
+        const int mine = (r.hi - r.lo + TM - 1) / TM;
         int inc = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -496,8 +496,8 @@ __device__ __forceinline__ int find_block(const Args& p, int block, int& lo, int
         const uint64_t past = __ballot(seen + inc > block);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
-            lo = __shfl(first, l) + (block - seen - __shfl(inc - mine, l)) * TM;
-            hi = __shfl(end, l);
+            lo = __shfl(r.lo, l) + (block - seen - __shfl(inc - mine, l)) * TM;
+            hi = __shfl(r.hi, l);
             return base + l;
         }
         seen += __shfl(inc, 63);
