@@ -109,13 +109,10 @@ struct Args : I4Mm {
 // The row of x that row m of y is made from, and whether a source names one that is there (a
 // row whose source is out of range gives zeros, and reads row 0 meanwhile).
 __device__ __forceinline__ bool x_row_ok(const Args& p, int m) {
-    return !p.src || (uint32_t)(p.src[m] / p.topk) < (uint32_t)p.x_rows;
+    return !p.src || source_row(p.src[m], p.topk, p.x_rows) >= 0;
 }
 __device__ __forceinline__ int64_t x_row(const Args& p, int m) {
-    if (!p.src)
-        return m;
-    const int r = p.src[m] / p.topk;
-    return (uint32_t)r < (uint32_t)p.x_rows ? r : 0;
+    return p.src ? max(source_row(p.src[m], p.topk, p.x_rows), 0) : m;
 }
 
 // One unit's data of one block of 16 rows of W: 256 columns are one 128-byte line of codes of

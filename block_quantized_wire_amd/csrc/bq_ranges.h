@@ -20,4 +20,10 @@ constexpr RowRange expert_rows(int32_t first, int32_t end, int32_t rows) {
     return RowRange{lo, end < lo ? lo : end < rows ? end : rows};
 }
 
+// The row of x that a slot's token is, or -1 where there is none.  The sign is tested before the
+// division, which rounds towards 0.
+constexpr int32_t source_row(int32_t slot, int32_t topk, int32_t x_rows) {
+    return slot < 0 || slot / topk >= x_rows ? -1 : slot / topk;
+}
+
 }  // namespace bq

@@ -144,7 +144,8 @@ bq_status bq_moe_combine_bwd_f32(const float* dy, int64_t lddy, const float* row
  * src is not NULL (the tokens unsorted; x_rows rows of x).  W_e is the I4 matrix of N rows
  * and K columns at c + e*stride_c, scale + e*stride_s, zero + e*stride_z (strides in
  * elements: at least N rows, stride_c % 16 == 0, the others % 4 == 0).  rows is the number of
- * rows of y (tokens*topk); rows outside every expert are not written.  topk is ignored
+ * rows of y (tokens*topk); rows outside every expert are not written, and a row whose source
+ * names no row of x (src negative, or too large) becomes 0.  topk is ignored
  * where src is NULL; x must then hold `rows` rows (x_rows >= rows). */
 bq_status bq_moe_mm_i4(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* src, int topk,
                        const int32_t* off, int experts, int64_t rows, const uint8_t* c,

@@ -53,3 +53,27 @@ def test_offsets_out_of_range(rows, n, kind):
         got = y.cpu()
         assert torch.equal(got[lo:hi], want[lo:hi]), off
         assert bool((got[:lo] == 5.0).all()) and bool((got[hi:] == 5.0).all()), off
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,n", SIZES)
+def test_sources_out_of_range(rows, n, kind):
+    """Sources that name no row of x give rows of zeros: those just below 0, which a division
+    by topk would bring to row 0, among them."""
+    say(f"moe_mm_i4 sources out of range: rows={rows} n={n} {kind}")
+    rng = np.random.default_rng([rows, n, 1])
+    topk, x_rows = 3, rows // 2
+    mats = [ref.matrix(rng, n, 128, 64, kind, True, exact=True)] * 4
+    x = torch.from_numpy(rng.integers(1, 4, (x_rows, 128))).to(ref.TORCH[kind])
+    src = rng.integers(0, x_rows * topk, rows)
+    bad = rng.random(rows) < 0.4
+    bad[:6] = True
+    src[bad] = rng.choice([-1, -2, -3, -4, MIN, x_rows * topk, MAX], int(bad.sum()))
+    src[:5] = [-1, -2, -3, MIN, x_rows * topk]
+    cut = rows // 4
+    off = [0, cut, 2 * cut, 3 * cut, rows]
+    y = torch.full((rows, n), 5.0, dtype=ref.TORCH[kind], device=DEV)
+    product(x, mats, off, torch.from_numpy(src.astype(np.int32)), topk, y, kind)
+    want = ref.rne(ref.product(x, *mats[0], 128, 64, kind)[0], kind)[np.where(bad, 0, src // topk)]
+    want[torch.from_numpy(bad)] = 0
+    assert torch.equal(y.cpu(), want)

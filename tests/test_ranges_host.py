@@ -50,3 +50,21 @@ int main() {
     return 0;
 }
 """)
+
+
+def test_a_source_names_a_row_of_x_or_none(tmp_path):
+    """A slot in [0, x_rows * topk) names row slot / topk; every other value names none, those
+    between -topk and 0 too."""
+    run(tmp_path, """
+int main() {
+    for (int32_t rows : kRows)
+        for (int32_t topk : {1, 2, 7, 64})
+            for (int32_t slot : kAny) {
+                const int32_t r = bq::source_row(slot, topk, rows);
+                const bool there = slot >= 0 && slot < (int64_t)rows * topk;
+                if (there ? r != slot / topk : r != -1)
+                    return printf("rows %d topk %d slot %d: row %d\\n", rows, topk, slot, r), 1;
+            }
+    return 0;
+}
+""")
