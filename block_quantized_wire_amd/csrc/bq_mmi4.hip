@@ -10,6 +10,15 @@
 // at most a factor of 16 + zero over |code - zero| in the rounding of binary32 sums.  (bf16
 // has no packed subtraction; binary16 has, and k_mm_i4 subtracts the zero point there.)
 //
+// Range.  A group's sums reach 128 * 31 |x|, which bf16's larger values would take out of
+// binary32 although the product itself is finite.  So bf16's operands are (16 + code) / 4096 and,
+// for sum x, 1 / 4096: no finite x overflows, and nothing is lost below, since x is a multiple
+// of 2^-133 and the products one of 2^-145, where binary32 ends at 2^-149 (the matrix cores
+// keep subnormals).  The factor comes back once, on a finished result: a power of two changes no
+// rounding of the sums, but results below about 2^-100 hold up to 2^-138 a group of error, and
+// the scales stay as they are, so that the largest ones do not overflow either.  Binary16 sums
+// stay below 2^28 as they are.
+//
 // Three kernels, chosen by the row counts (launch_shape): k_ms_i4 for up to 16 rows, bound by the
 // bytes of the weights; k_mv_i4 for more in products that keep few workgroups busy, bound by
 // the making of operands; and k_mm_i4, bound by the matrix cores and the vector
@@ -27,6 +36,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kUnit = 256;       // columns of a unit: 128 bytes of codes of a row
+
+// What the sums of x are made with (two to a word): 1, or bf16's 2^-12.
+template <bool F16>
+constexpr uint32_t kOnes = F16 ? 0x3C003C00u : 0x39803980u;
 
 template <bool F16>
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
@@ -54,16 +67,22 @@ __device__ __forceinline__ uint16_t from_f32(float f) {
         return (uint16_t)pack_bf16x2(f, 0.0f);
 }
 
-// The 8 codes of a word as operands 16 + code, in the order 0,4, 1,5, 2,6, 3,7 (codes i and
-// i+4 are 16 bits apart).  The code's bits go to the top of the significand: bits 3..6 of
-// a bf16 16.0 (0x4180), bits 6..9 of a binary16 16.0 (0x4C00).  The mask and the base are held
+// A finished sum, back at its size and rounded.
+template <bool F16>
+__device__ __forceinline__ uint16_t result(float sum) {
+    return from_f32<F16>(F16 ? sum : sum * 4096.0f);
+}
+
+// The 8 codes of a word as operands 16 + code (bf16: over 4096), in the order 0,4, 1,5, 2,6, 3,7
+// (codes i and i+4 are 16 bits apart).  The code's bits go to the top of the significand: bits
+// 3..6 of a bf16 2^-8 (0x3B80), bits 6..9 of a binary16 16.0 (0x4C00).  The mask and the base are held
 // in registers, so that the two steps are one shift and one and-or (an instruction takes no
 // two literals).
 template <bool F16>
 struct Codes {
     uint32_t mask, base;
     __device__ __forceinline__ Codes()
-        : mask(F16 ? 0x03C003C0u : 0x00780078u), base(F16 ? 0x4C004C00u : 0x41804180u) {
+        : mask(F16 ? 0x03C003C0u : 0x00780078u), base(F16 ? 0x4C004C00u : 0x3B803B80u) {
         asm("" : "+s"(mask));
         asm("" : "+v"(base));
     }
@@ -219,8 +238,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
         sr[r] = s + n * p.lds;
         zr[r] = Z ? z + n * p.ldz : nullptr;
     }
-    constexpr uint32_t kOne = F16 ? 0x3C003C00u : 0x3F803F80u;
-    const u32x4 ones{kOne, kOne, kOne, kOne};
+    const u32x4 ones{kOnes<F16>, kOnes<F16>, kOnes<F16>, kOnes<F16>};
     const Codes<F16> codes;
 
     for (int m0 = lo; m0 < hi; m0 += stride) {
@@ -360,7 +378,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
             const int i = u % NI, t = u / NI % MT, r = u / (NI * MT);
             const int m = m0 + 16 * t + g + 4 * i, n = n0 + 16 * r + n16;
             if (m < hi && n < p.N)
-                p.y[m * p.ldy + n] = from_f32<F16>(x_row_ok(p, m) ? v : 0.0f);
+                p.y[m * p.ldy + n] = result<F16>(x_row_ok(p, m) ? v : 0.0f);
         }
         __syncthreads();
     }
@@ -430,15 +448,15 @@ static_assert(sizeof(TileShared<32, true, false, 128, 256>) <= 80 * 1024, "LDS o
 
 // The 8 codes of a word as operands in column order, less the zero point where the type has
 // a packed subtraction.  Codes 2i, 2i+1 are byte i of the even and of the odd nibbles.
-//  bf16: 16 + code.  The code's bits sit in the low byte under a set bit 7; the high byte is
-//        0x41 (16.0 is 0x4180).
+//  bf16: (16 + code) / 4096.  The code's bits sit in the low byte under a set bit 7; the high
+//        byte is 0x3B (2^-8 is 0x3B80).
 //  binary16: (code - zero) / 512, exactly.  A byte by itself is the subnormal code * 2^-24; one
 //        packed fused multiply-add by 2^15 makes it normal and subtracts the zero point.
 template <bool F16>
 struct TileCodes {
     uint32_t mask, set, high;
     __device__ __forceinline__ TileCodes()
-        : mask(F16 ? 0x0F0F0F0Fu : 0x78787878u), set(0x80808080u), high(0x41414141u) {
+        : mask(F16 ? 0x0F0F0F0Fu : 0x78787878u), set(0x80808080u), high(0x3B3B3B3Bu) {
         asm("" : "+s"(mask));
         asm("" : "+v"(set));
         asm("" : "+s"(high));
@@ -596,7 +614,7 @@ __global__ __launch_bounds__((64 * kTileWaves<TM, TN> * kTileParts<TN>), TM == 1
     // bf16: the sums of x per row and group of a stage, each wave its share of the blocks of rows
     // (negative, and times the 24 of the constant zero point, where the products start from them)
     const auto sums_of_x = [&](const Stage& t) {
-        const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        const u32x4 ones{kOnes<F16>, kOnes<F16>, kOnes<F16>, kOnes<F16>};
         for (int block = wave; block < kMB; block += kWaves) {
             f32x4 a = mma<F16>(x_at(t, block, 0), ones, f32x4{});
             f32x4 b = mma<F16>(x_at(t, block, 1), ones, kHalves == 2 ? f32x4{} : a);
@@ -769,7 +787,7 @@ __global__ __launch_bounds__((64 * kTileWaves<TM, TN> * kTileParts<TN>), TM == 1
         const auto compute_read = [&](Inputs& in, int stage, int q, int unit) {
             Operands o;
             make(o, in.raw, stage, q, unit);
-            const u32x4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            const u32x4 ones{kOnes<F16>, kOnes<F16>, kOnes<F16>, kOnes<F16>};
             f32x4 xs[kMB][kHalves], acc[kMB][kNB][kHalves];
 #pragma unroll
             for (int m = 0; m < kMB; ++m)
@@ -903,7 +921,7 @@ __global__ __launch_bounds__((64 * kTileWaves<TM, TN> * kTileParts<TN>), TM == 1
                 for (int b = 0; b < kNB; ++b) {
                     const int n = n0 + wave * kWaveN + 16 * b + n16;
                     if (n < p.N)
-                        p.y[row * p.ldy + n] = from_f32<F16>(ok ? sum[m][b][i] : 0.0f);
+                        p.y[row * p.ldy + n] = result<F16>(ok ? sum[m][b][i] : 0.0f);
                 }
             }
         }
@@ -969,8 +987,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * R;
     const int groups = p.K / G;
-    constexpr uint32_t kOne = F16 ? 0x3C003C00u : 0x3F803F80u;
-    const u32x4 ones{kOne, kOne, kOne, kOne};
+    const u32x4 ones{kOnes<F16>, kOnes<F16>, kOnes<F16>, kOnes<F16>};
     const Codes<F16> codes;
     // Addresses are a uniform base that moves with the unit and a lane's 32-bit offset, which
     // the launch has checked to be enough.  First what this lane brings of the weights.
@@ -1120,7 +1137,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
                 v += reinterpret_cast<const float*>(ring[w])[u * 64 + lane];
             const int m = m0 + g + 4 * (u % NI), n = n0 + 16 * (u / NI) + n16;
             if (m < p.rows && n < p.N)
-                p.y[m * p.ldy + n] = from_f32<F16>(v);
+                p.y[m * p.ldy + n] = result<F16>(v);
         }
         __syncthreads();
     }

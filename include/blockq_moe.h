@@ -59,7 +59,9 @@ bq_status bq_dequant_i4_f16(const uint8_t* c, int64_t ldc, const uint16_t* scale
  * a group are taken in binary32 by the matrix cores from exact products (of x and code -
  * zero, or of x and 16 + code and of x alone, subtracted afterwards), the group's scale is
  * applied to them in binary32, and y is rounded once.  The same call gives the same bits;
- * the order of the sums depends on the sizes.  M == 0 or N == 0
+ * the order of the sums depends on the sizes.  No finite x overflows a group's sums (bf16 takes
+ * them at 2^-12 of their size), so y is finite where the sum over the groups is; bf16 results
+ * below about 2^-100 hold an absolute error of up to 2^-138 a group.  M == 0 or N == 0
  * launches nothing; K must be positive, M and K at most 2^30 and N at most 2^26 (else
  * BQ_ERR_SIZE).  y must not overlap an input.  _f16: X, scale and
  * Y are binary16. */
