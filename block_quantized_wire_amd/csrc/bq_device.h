@@ -218,15 +218,15 @@ __device__ __forceinline__ uint32_t pack_lo_bytes(uint32_t a, uint32_t b, uint32
     return lo | hi;
 }
 
-// fl64(1/s) to within 2^-52 (relative) for a positive finite binary32 s: the hardware
+// fl64(1/s) to within 2^-52 (relative) for a positive s of binary32 size: the hardware
 // fp64 reciprocal refined by two Newton-Raphson steps (each squares the error).
-__device__ __forceinline__ double recip64(float s) {
-    const double d = (double)s;
-    double r = __builtin_amdgcn_rcp(d);
-    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
-    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+__device__ __forceinline__ double recip64(double s) {
+    double r = __builtin_amdgcn_rcp(s);
+    r = __builtin_fma(r, __builtin_fma(-s, r, 1.0), r);
+    r = __builtin_fma(r, __builtin_fma(-s, r, 1.0), r);
     return r;
 }
+__device__ __forceinline__ double recip64(float s) { return recip64((double)s); }
 
 // fl32(x / s) exactly (see the header comment), given r = recip64(s).
 __device__ __forceinline__ float quot32(float x, double r) { return (float)((double)x * r); }

@@ -6,9 +6,9 @@
  * on streams, errors (bq_status), ownership, aliasing, the 2^48 byte limit on an operand's
  * span, and device and host pointers.  In place calls are not allowed: every output is apart
  * from every input.  Where a size makes the result empty, OK is returned, nothing is launched
- * and no pointer is read, unless an entry says otherwise.  Non-finite values follow IEEE
- * arithmetic within the row they are in (a row of x with a NaN or an infinity gives a row of
- * unspecified non-finite or finite values) and do not reach other rows.
+ * and no pointer is read, unless an entry says otherwise.  Unlike blockq.h's codecs these
+ * entries take non-finite values: the moved and summed rows follow IEEE arithmetic, the 4-bit
+ * codec and products as stated there, and no value reaches the results of another row.
  */
 #ifndef BLOCKQ_MOE_H
 #define BLOCKQ_MOE_H
@@ -36,7 +36,9 @@ extern "C" {
 
 /* bf16 rows -> I4 codes and scales, symmetric (zero point 8).  Per group: amax = max |x|;
  * scale = bf16_rne(fl32(amax / 7)); code = 8 + q, q = round-half-even(fl32(x / scale))
- * clamped to [-7, 7]; q = 0 where the scale is +0.  x: bf16[rows][ldx], 16-byte aligned,
+ * clamped to [-7, 7]; q = 0 where the scale is +0.  A NaN in a group makes its scale NaN and
+ * its codes 8; without one, an infinity makes the scale +inf, infinities q = 7 and -7 and
+ * finite values q = 0 (so that they come back as themselves and as NaN).  x: bf16[rows][ldx], 16-byte aligned,
  * ldx >= cols, ldx % 8 == 0.  Entries of c and scale beyond a row's columns and groups are
  * not written.  rows * cols / 8 < 2^32.  _f16: x and scale are IEEE binary16 (scale =
  * f16_rne(fl32(amax / 7))). */
@@ -61,7 +63,9 @@ bq_status bq_dequant_i4_f16(const uint8_t* c, int64_t ldc, const uint16_t* scale
  * applied to them in binary32, and y is rounded once.  The same call gives the same bits;
  * the order of the sums depends on the sizes.  No finite x overflows a group's sums (bf16 takes
  * them at 2^-12 of their size), so y is finite where the sum over the groups is; bf16 results
- * below about 2^-100 hold an absolute error of up to 2^-138 a group.  M == 0 or N == 0
+ * below about 2^-100 hold an absolute error of up to 2^-138 a group.  A NaN or an infinity in a
+ * row of x makes every value of that row of y NaN or infinite, one among a row's scales every
+ * value of that column.  M == 0 or N == 0
  * launches nothing; K must be positive, M and K at most 2^30 and N at most 2^26 (else
  * BQ_ERR_SIZE).  y must not overlap an input.  _f16: X, scale and
  * Y are binary16. */
