@@ -111,16 +111,18 @@ for _name in ("bq_quant_i4", "bq_dequant_i4", "bq_mm_i4", "bq_moe_mm_i4", "bq_mo
 for _name in ("bq_moe_combine", "bq_moe_combine_bwd"):
     _SIGS[_name + "_f32"] = _SIGS[_name]
 _lib = None
+_i32 = _f32 = None      # torch's types, known once the library is loaded
 
 
 def _L() -> ctypes.CDLL:
     """The loaded libblockq.so (loaded on first use; a missing library is an error)."""
-    global _lib
+    global _lib, _i32, _f32
     if _lib is None:
         # torch brings its own HIP runtime (same soname, libamdhip64.so.7).  Loading it
         # first makes libblockq.so bind to that one runtime; loaded the other way round,
         # the process would hold two HIP runtimes and ours would see no device.
-        import torch  # noqa: F401
+        import torch
+        _i32, _f32 = torch.int32, torch.float32
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python block_quantized_wire_amd/build.py` (hipcc, gfx950)")
@@ -574,7 +576,32 @@ def bq_mm_i4_f16(x, c, scale, y, zero=None, group: int = 128, M: int | None = No
 # ---- the expert layer: tokens sorted by expert, expert products, and back ---------------
 #
 # off (experts + 1), src and pos (tokens * topk): torch.int32, as bq_moe_sort writes them;
-# weight and dweight (tokens, topk): torch.float32, contiguous.
+# weight and dweight (tokens, topk): torch.float32, contiguous.  Other types (the int64 of
+# torch.topk's ids, weights in bf16) are a TypeError, other layouts and arrays that are too
+# short a ValueError: their bytes would be read as something else, or past their end.  An
+# address in place of such a tensor is passed on as it is.
+
+def _refuse(fn: str, *arrays) -> None:
+    """Raise for the first of (name, tensor, type, least entries) that is not what it should be.
+    The calls look at their arrays in one expression and come here only where that fails: a
+    call costs the host a few microseconds, and a function for each array one more."""
+    for arg, t, dtype, size in arrays:
+        if isinstance(t, int):
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{fn}: {arg} is {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {arg} is not contiguous")
+        if t.numel() < size:
+            raise ValueError(f"{fn}: {arg} has {t.numel()} of {size} entries")
+
+
+def _one_choice(fn: str, slots, tokens: int) -> int:
+    """topk where it was left out: 1, if that is what an array with an entry per slot says."""
+    if not isinstance(slots, int) and slots.numel() != tokens:
+        raise ValueError(f"{fn}: topk is needed for {slots.numel()} slots of {tokens} tokens")
+    return 1
+
 
 def bq_moe_sort_ws_bytes(tokens: int, topk: int, experts: int) -> int:
     """Scratch bytes of bq_moe_sort (-1 for sizes outside its limits)."""
@@ -584,53 +611,105 @@ def bq_moe_sort_ws_bytes(tokens: int, topk: int, experts: int) -> int:
 def bq_moe_sort(expert, experts: int, off, src, pos, ws=None, stream=None) -> None:
     """expert (tokens, topk) torch.int32, contiguous -> off, src, pos; ws: scratch of at least
     bq_moe_sort_ws_bytes bytes, or None where that is 0."""
+    lib, i32 = _L(), _i32
     tokens, topk = expert.shape
+    slots = tokens * topk
+    try:
+        fits = (expert.dtype is i32 and off.dtype is i32 and src.dtype is i32 and pos.dtype is i32
+                and expert.is_contiguous() and off.is_contiguous() and src.is_contiguous()
+                and pos.is_contiguous() and off.numel() > experts and src.numel() >= slots
+                and pos.numel() >= slots)
+    except AttributeError:      # an address
+        fits = False
+    if not fits:
+        _refuse("bq_moe_sort", ("expert", expert, i32, 0), ("off", off, i32, experts + 1),
+                ("src", src, i32, slots), ("pos", pos, i32, slots))
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("bq_moe_sort", _L().bq_moe_sort(_ptr(expert), tokens, topk, experts, _ptr(off),
-                                           _ptr(src), _ptr(pos), _ptr(ws), ws_bytes,
-                                           _stream(stream)))
+    _check("bq_moe_sort", lib.bq_moe_sort(expert.data_ptr(), tokens, topk, experts, _ptr(off),
+                                          _ptr(src), _ptr(pos), _ptr(ws), ws_bytes,
+                                          _stream(stream)))
 
 
 def bq_moe_gather(x, pos, off, out, topk: int, cols: int | None = None, stream=None) -> None:
     """out[pos[t*topk + j]] = x[t]; the rows of dropped slots become 0."""
-    cols = x.shape[1] if cols is None else cols
+    lib, i32 = _L(), _i32
+    shape, bounds = x.shape, off.numel()
+    tokens = shape[0]
+    try:
+        fits = (pos.dtype is i32 and off.dtype is i32 and pos.is_contiguous()
+                and off.is_contiguous() and pos.numel() >= tokens * topk)
+    except AttributeError:      # an address
+        fits = False
+    if not fits:
+        _refuse("bq_moe_gather", ("pos", pos, i32, tokens * topk), ("off", off, i32, 0))
     _check("bq_moe_gather",
-           _L().bq_moe_gather(_ptr(x), x.stride(0), _ptr(pos), _ptr(off), x.shape[0], topk,
-                              off.shape[0] - 1, cols, x.element_size(), _ptr(out), out.stride(0),
-                              _stream(stream)))
+           lib.bq_moe_gather(x.data_ptr(), x.stride()[0], _ptr(pos), off.data_ptr(), tokens, topk,
+                             bounds - 1, shape[1] if cols is None else cols, x.element_size(),
+                             out.data_ptr(), out.stride()[0], _stream(stream)))
 
 
 def _moe_combine(name, rows, pos, off, y, weight, topk, cols, stream):
-    cols = y.shape[1] if cols is None else cols
-    _check(name, getattr(_L(), name)(_ptr(rows), rows.stride(0), _ptr(pos), _ptr(off),
-                                     _ptr(weight), y.shape[0], topk, off.shape[0] - 1, cols,
-                                     _ptr(y), y.stride(0), _stream(stream)))
+    lib, i32 = _L(), _i32
+    shape, bounds = y.shape, off.numel()
+    tokens = shape[0]
+    if topk is None:
+        wshape = getattr(weight, "shape", ())
+        topk = wshape[1] if len(wshape) == 2 else _one_choice(name, pos if weight is None else weight,
+                                                            tokens)
+    slots = tokens * topk
+    try:
+        fits = (pos.dtype is i32 and off.dtype is i32 and pos.is_contiguous()
+                and off.is_contiguous() and pos.numel() >= slots
+                and (weight is None or weight.dtype is _f32 and weight.is_contiguous()
+                     and weight.numel() >= slots))
+    except AttributeError:      # an address
+        fits = False
+    if not fits:
+        _refuse(name, ("pos", pos, i32, slots), ("off", off, i32, 0),
+                ("weight", 0 if weight is None else weight, _f32, slots))
+    _check(name, getattr(lib, name)(rows.data_ptr(), rows.stride()[0], _ptr(pos), off.data_ptr(),
+                                    _ptr(weight), tokens, topk, bounds - 1,
+                                    shape[1] if cols is None else cols, y.data_ptr(), y.stride()[0],
+                                    _stream(stream)))
 
 
-def bq_moe_combine(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+def bq_moe_combine(rows, pos, off, y, weight=None, topk: int | None = None, cols: int | None = None,
                    stream=None) -> None:
     """y[t] = sum over kept j of weight[t, j] * rows[pos[t*topk + j]] (weight None: 1, which is
-    the gradient of bq_moe_gather)."""
+    the gradient of bq_moe_gather).  topk may be left out where weight is (tokens, topk) or a
+    token has one slot."""
     _moe_combine("bq_moe_combine", rows, pos, off, y, weight, topk, cols, stream)
 
 
-def bq_moe_combine_f16(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+def bq_moe_combine_f16(rows, pos, off, y, weight=None, topk: int | None = None, cols: int | None = None,
                        stream=None) -> None:
     _moe_combine("bq_moe_combine_f16", rows, pos, off, y, weight, topk, cols, stream)
 
 
-def bq_moe_combine_f32(rows, pos, off, y, weight=None, topk: int = 1, cols: int | None = None,
+def bq_moe_combine_f32(rows, pos, off, y, weight=None, topk: int | None = None, cols: int | None = None,
                        stream=None) -> None:
     _moe_combine("bq_moe_combine_f32", rows, pos, off, y, weight, topk, cols, stream)
 
 
 def _moe_combine_bwd(name, dy, rows, pos, off, weight, drows, dweight, cols, stream):
-    cols = dy.shape[1] if cols is None else cols
+    lib, i32, f32 = _L(), _i32, _f32
     tokens, topk = weight.shape
-    _check(name, getattr(_L(), name)(_ptr(dy), dy.stride(0), _ptr(rows), rows.stride(0), _ptr(pos),
-                                     _ptr(off), _ptr(weight), tokens, topk, off.shape[0] - 1, cols,
-                                     _ptr(drows), drows.stride(0), _ptr(dweight),
-                                     _stream(stream)))
+    bounds, slots = off.numel(), tokens * topk
+    try:
+        fits = (pos.dtype is i32 and off.dtype is i32 and weight.dtype is f32
+                and dweight.dtype is f32 and pos.is_contiguous() and off.is_contiguous()
+                and weight.is_contiguous() and dweight.is_contiguous() and pos.numel() >= slots
+                and dweight.numel() >= slots)
+    except AttributeError:      # an address
+        fits = False
+    if not fits:
+        _refuse(name, ("pos", pos, i32, slots), ("off", off, i32, 0), ("weight", weight, f32, 0),
+                ("dweight", dweight, f32, slots))
+    _check(name, getattr(lib, name)(dy.data_ptr(), dy.stride()[0], rows.data_ptr(),
+                                    rows.stride()[0], _ptr(pos), off.data_ptr(),
+                                    weight.data_ptr(), tokens, topk, bounds - 1,
+                                    dy.shape[1] if cols is None else cols, drows.data_ptr(),
+                                    drows.stride()[0], _ptr(dweight), _stream(stream)))
 
 
 def bq_moe_combine_bwd(dy, rows, pos, off, weight, drows, dweight, cols: int | None = None,
@@ -653,24 +732,43 @@ def bq_moe_combine_bwd_f32(dy, rows, pos, off, weight, drows, dweight, cols: int
 
 
 def _moe_mm_i4(name, x, off, c, scale, y, zero, group, src, topk, N, K, stream):
-    N = y.shape[1] if N is None else N
-    K = x.shape[1] if K is None else K
-    ldz, stride_z = (0, 0) if zero is None else (zero.stride(1), zero.stride(0))
-    _check(name, getattr(_L(), name)(_ptr(x), x.stride(0), x.shape[0], _ptr(src), topk, _ptr(off),
-                                     off.shape[0] - 1, y.shape[0], _ptr(c), c.stride(1),
-                                     c.stride(0), _ptr(scale), scale.stride(1), scale.stride(0),
-                                     _ptr(zero), ldz, stride_z, N, K, group, _ptr(y), y.stride(0),
-                                     _stream(stream)))
+    lib, i32 = _L(), _i32
+    x_shape, y_shape, bounds = x.shape, y.shape, off.numel()
+    x_rows, rows = x_shape[0], y_shape[0]
+    if src is None:
+        topk = 1
+        fits = off.dtype is i32 and off.is_contiguous()
+    else:
+        if topk is None:
+            topk = _one_choice(name, src, x_rows)
+        try:
+            fits = (off.dtype is i32 and src.dtype is i32 and off.is_contiguous()
+                    and src.is_contiguous())
+            rows = min(rows, src.numel())   # a longer y has rows of no expert at its end
+        except AttributeError:      # an address
+            fits = False
+    if not fits:
+        _refuse(name, ("off", off, i32, 0), ("src", 0 if src is None else src, i32, 0))
+    c_strides, s_strides = c.stride(), scale.stride()
+    z_strides = (0, 0) if zero is None else zero.stride()
+    _check(name, getattr(lib, name)(x.data_ptr(), x.stride()[0], x_rows, _ptr(src), topk,
+                                    off.data_ptr(), bounds - 1, rows, c.data_ptr(), c_strides[1],
+                                    c_strides[0], scale.data_ptr(), s_strides[1], s_strides[0],
+                                    _ptr(zero), z_strides[1], z_strides[0],
+                                    y_shape[1] if N is None else N,
+                                    x_shape[1] if K is None else K, group,
+                                    y.data_ptr(), y.stride()[0], _stream(stream)))
 
 
-def bq_moe_mm_i4(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int = 1,
+def bq_moe_mm_i4(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int | None = None,
                  N: int | None = None, K: int | None = None, stream=None) -> None:
     """y[p] = bf16(X_p W_e^T) for the sorted rows p of every expert e: X_p = x[p], or
-    x[src[p] // topk] where src is given.  c, scale, zero: (experts, N, ...)."""
+    x[src[p] // topk] where src is given.  c, scale, zero: (experts, N, ...).  topk may be left
+    out without src, and where a token has one slot."""
     _moe_mm_i4("bq_moe_mm_i4", x, off, c, scale, y, zero, group, src, topk, N, K, stream)
 
 
-def bq_moe_mm_i4_f16(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int = 1,
+def bq_moe_mm_i4_f16(x, off, c, scale, y, zero=None, group: int = 128, src=None, topk: int | None = None,
                      N: int | None = None, K: int | None = None, stream=None) -> None:
     """bq_moe_mm_i4 on IEEE binary16 x, scale and y."""
     _moe_mm_i4("bq_moe_mm_i4_f16", x, off, c, scale, y, zero, group, src, topk, N, K, stream)
