@@ -121,7 +121,6 @@ __device__ __forceinline__ u32x4 exchange(u32x4 q) {
 
 struct Args : I4Mm {
     int32_t units;      // ceil(K / 256)
-    int32_t chunk;      // row chunks between two of a workgroup's (dense)
     int32_t block0;     // first row block of a launch of many
 };
 
@@ -197,31 +196,31 @@ __device__ __forceinline__ void wait_and_join() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Few rows of x: the bytes of the weights bound this kernel, so it streams them once, straight
-// into registers, D units of 256 columns ahead.  A workgroup takes R blocks of 16 weight rows
-// and KW waves that take the units in turn; their sums meet in LDS in wave order.
-// NI results per lane and block of 16 tokens: the token of lane quarter g's result i is
-// g + 4i, so up to 4 tokens need one result per lane, up to 8 two.  MT > 1 only with NI = 4.
+// Few rows of x, by expert or more than 16 of them: the weights go straight into registers, one
+// unit of 256 columns at a time; what covers a unit's loads are the other waves of the compute
+// unit.  A workgroup takes R blocks of 16 weight rows and KW waves that take the units in turn;
+// their sums meet in LDS in wave order.  A wave's products take MT blocks of 16 rows of x; dense
+// rows beyond them are other workgroups', an expert's are this one's next.  Operand row n16 of a
+// block is token n16 / 4 + 4 (n16 % 4), so that lane quarter g holds the results of tokens g + 4i.
 // Tail: K is not a multiple of 256.  The columns that the last unit lacks are whole groups:
 // their loads are moved to columns that are there, and the groups are left out.
-template <bool F16, int G, bool Z, bool Tail, int NI, int MT, int R, int KW, int D>
+template <bool F16, int G, bool Z, bool Tail, int MT, int R, int KW>
 __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) void k_mv_i4(Args p) {
     constexpr int kGroups = kUnit / G, kPer = 8 / kGroups;
-    constexpr int kTokens = 16 * (MT - 1) + 4 * NI;
-    __shared__ float red[KW][R * MT * NI][64];
+    constexpr int kTokens = 16 * MT;
+    __shared__ float red[KW][R * MT * 4][64];
     const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * R;
     const uint8_t* c = p.c;
     const uint16_t* s = p.s;
     const uint8_t* z = p.z;
-    int lo = blockIdx.y * kTokens, hi = p.rows, stride = p.chunk * kTokens;
+    int lo = blockIdx.y * kTokens, hi = min(p.rows, lo + kTokens);
     if (p.off) {
         const int e = blockIdx.y;
         const RowRange r = expert_rows(p.off[e], p.off[e + 1], p.rows);
         lo = r.lo;
         hi = r.hi;
-        stride = kTokens;
         c += e * p.stride_c;
         s += e * p.stride_s;
         z += e * p.stride_z;
@@ -241,13 +240,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const u32x4 ones{kOnes<F16>, kOnes<F16>, kOnes<F16>, kOnes<F16>};
     const Codes<F16> codes;
 
-    for (int m0 = lo; m0 < hi; m0 += stride) {
-        // the row of x of operand row n16 of each block of tokens: token n16 / 4 + 4 (n16 % 4);
-        // operand rows without a token repeat a token's, and their results are never stored
+    for (int m0 = lo; m0 < hi; m0 += kTokens) {
+        // operand rows without a token repeat the last one's, and their results are never stored
         const uint16_t* xr[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const int m = m0 + 16 * t + (n16 >> 2) + 4 * ((n16 & 3) % NI);
+            const int m = m0 + 16 * t + (n16 >> 2) + 4 * (n16 & 3);
             xr[t] = p.x + x_row(p, min(m, hi - 1)) * p.ldx;
         }
         const auto load = [&](Buf<G, Z, MT, R>& b, int unit) {
@@ -262,16 +260,16 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
                     b.x[t][j] = ld16(xr[t] + (Tail ? min(col, p.K - 8) : col));
                 }
             }
-            // left alone, the compiler gathers the loads of all D units behind the last product
+            // left alone, the compiler moves these loads among the products before them
             __builtin_amdgcn_sched_barrier(0);
         };
-        float sum[R][MT][NI];
+        float sum[R][MT][4];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
+                for (int i = 0; i < 4; ++i)
                     sum[r][t][i] = 0.0f;
 
         const auto compute = [&](Buf<G, Z, MT, R>& b, int unit) {
@@ -316,7 +314,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int i = 0; i < NI; ++i)
+                        for (int i = 0; i < 4; ++i)
                             sum[r][t][i] = __builtin_fmaf(
                                 scale, __builtin_fmaf(-zero, xs[t][i], acc[r][t][i]), sum[r][t][i]);
                 }
@@ -329,37 +327,20 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
+                    for (int i = 0; i < 4; ++i)
                         asm volatile("" : "+v"(sum[r][t][i]));
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        // D units are in flight.  The main loop has no branches, so that a unit waits for its own
-        // loads only; the last 2 D - 1 units at most are taken one by one.
         if (wave < p.units) {
-            Buf<G, Z, MT, R> buf[D];
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-                load(buf[d], min(wave + d * KW, p.units - 1));
+            Buf<G, Z, MT, R> buf;
+            load(buf, wave);
             int k = wave;
-            for (; k + (2 * D - 1) * KW < p.units; k += D * KW) {
-#pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    compute(buf[d], k + d * KW);
-                    load(buf[d], k + (d + D) * KW);
-                }
+            for (; k + KW < p.units; k += KW) {
+                compute(buf, k);
+                load(buf, k + KW);
             }
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (k + d * KW < p.units)
-                    compute(buf[d], k + d * KW);
-                if (k + (d + D) * KW < p.units)
-                    load(buf[d], k + (d + D) * KW);
-            }
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-                if (k + (d + D) * KW < p.units)
-                    compute(buf[d], k + (d + D) * KW);
+            compute(buf, k);
         }
 
 #pragma unroll
@@ -367,15 +348,15 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    red[wave][(r * MT + t) * NI + i][lane] = sum[r][t][i];
+                for (int i = 0; i < 4; ++i)
+                    red[wave][(r * MT + t) * 4 + i][lane] = sum[r][t][i];
         __syncthreads();
-        for (int u = wave; u < R * MT * NI; u += KW) {
+        for (int u = wave; u < R * MT * 4; u += KW) {
             float v = red[0][u][lane];
 #pragma unroll
             for (int w = 1; w < KW; ++w)
                 v += red[w][u][lane];
-            const int i = u % NI, t = u / NI % MT, r = u / (NI * MT);
+            const int i = u % 4, t = u / 4 % MT, r = u / (4 * MT);
             const int m = m0 + 16 * t + g + 4 * i, n = n0 + 16 * r + n16;
             if (m < hi && n < p.N)
                 p.y[m * p.ldy + n] = result<F16>(x_row_ok(p, m) ? v : 0.0f);
@@ -943,14 +924,11 @@ hipError_t launch_tile(const Args& a0, hipStream_t st) {
     return e;
 }
 
-template <bool F16, int G, bool Z, bool Tail, int NI, int MT, int R, int KW, int D>
-hipError_t launch_mv(const Args& a0, hipStream_t st) {
-    Args a = a0;
-    constexpr int kTokens = 16 * (MT - 1) + 4 * NI;
-    const int64_t chunks = ((int64_t)a.rows + kTokens - 1) / kTokens;
-    a.chunk = (int32_t)(chunks < 16384 ? chunks : 16384);
-    const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), a.off ? a.experts : a.chunk);
-    return launch1(k_mv_i4<F16, G, Z, Tail, NI, MT, R, KW, D>, grid, dim3(64 * KW), st, a);
+template <bool F16, int G, bool Z, bool Tail, int MT, int R, int KW>
+hipError_t launch_mv(const Args& a, hipStream_t st) {
+    const int chunks = (a.rows + 16 * MT - 1) / (16 * MT);
+    const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), a.off ? a.experts : chunks);
+    return launch1(k_mv_i4<F16, G, Z, Tail, MT, R, KW>, grid, dim3(64 * KW), st, a);
 }
 
 // ---- few rows, staged through LDS -----------------------------------------------------------
@@ -959,7 +937,8 @@ hipError_t launch_mv(const Args& a0, hipStream_t st) {
 // loads.  A matrix operand wants 16 different rows in 16 adjacent lanes, and a load in that
 // order touches 16 lines of memory for every 256 bytes; through LDS each load instruction reads
 // whole lines.  A wave keeps to itself: its own units of 256 columns, its own ring of D units,
-// no barriers until the sums meet.  4 NI rows of x (NI = 1, 2 or 4) at a time.
+// no barriers until the sums meet.  x has up to 4 NI rows (NI = 1, 2 or 4): a lane has NI results
+// for each block of 16 rows of W, result i of lane quarter g that of token g + 4i.
 // Measured at 16 x 7168 x 43008, group 64 with zero points (170 MB, 35 us at the rate of a large
 // copy): 57 us, against 76 with loads to registers.  Units of 128 columns, which leave room
 // for 8 waves, take 70 (runs of 64 bytes); pairs of waves that share a unit's x and meet at a
@@ -979,7 +958,7 @@ struct alignas(16) Staged {
 template <bool F16, int G, bool Z, bool Tail, int NI, int R, int KW, int D>
 __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) void k_ms_i4(Args p) {
     using St = Staged<G, Z, NI, R>;
-    constexpr int kGroups = kUnit / G, kPer = 8 / kGroups, kTokens = 4 * NI;
+    constexpr int kGroups = kUnit / G, kPer = 8 / kGroups;
     constexpr int kS = St::kS, kZ = St::kZ;
     __shared__ St ring[KW][D];
     static_assert(sizeof(St) * D >= R * NI * 64 * 4, "the sums fit a wave's ring");
@@ -1007,153 +986,146 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const uint16_t* s0 = p.s + n0 * p.lds;
     const uint8_t* z0 = Z ? p.z + n0 * p.ldz : nullptr;
 
-    for (int m0 = blockIdx.y * kTokens; m0 < p.rows; m0 += p.chunk * kTokens) {
-        uint32_t xo[2 * NI], xk[2 * NI];       // values
+    uint32_t xo[2 * NI], xk[2 * NI];       // values
 #pragma unroll
-        for (int i = 0; i < 2 * NI; ++i) {
-            const int r = 2 * i + (lane >> 5);
-            xo[i] = (uint32_t)(min(r, p.rows - 1 - m0) * p.ldx);
-            xk[i] = 8 * ((lane & 31) ^ (r & 7));
+    for (int i = 0; i < 2 * NI; ++i) {
+        const int r = 2 * i + (lane >> 5);
+        xo[i] = (uint32_t)(min(r, p.rows - 1) * p.ldx);
+        xk[i] = 8 * ((lane & 31) ^ (r & 7));
+    }
+    const auto issue = [&](int unit, int slot) {
+        St& t = ring[wave][slot];
+        const uint32_t k = unit * kUnit, left = p.K - k;    // columns from here on
+        const uint8_t* cu = c0 + k / 2;
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i)
+            lds_load16(cu + (co[i] + (Tail ? min(wk, left / 2 - 16) : wk)), t.w + 1024 * i);
+        const uint16_t* xu = p.x + k;
+#pragma unroll
+        for (int i = 0; i < 2 * NI; ++i)
+            lds_load16(xu + (xo[i] + (Tail ? min(xk[i], left - 8) : xk[i])), t.x + 1024 * i);
+        // scales two to a word, zero points four; a word past the last group repeats its word
+        const uint32_t first = unit * kGroups, at4 = first & ~3u;
+        const uint32_t end2 = ((groups - 1) & ~1u) - first, end4 = ((groups - 1) & ~3u) - at4;
+        const uint16_t* su = s0 + first;
+#pragma unroll
+        for (int i = 0; i < St::kSLoads; ++i) {
+            const uint32_t w = 2 * ((64 * i + lane) % kS);
+            lds_load4(su + (so[i] + (Tail ? min(w, end2) : w)), t.s + 64 * i);
         }
-        const uint16_t* x0 = p.x + m0 * p.ldx;
-        const auto issue = [&](int unit, int slot) {
-            St& t = ring[wave][slot];
-            const uint32_t k = unit * kUnit, left = p.K - k;    // columns from here on
-            const uint8_t* cu = c0 + k / 2;
+        if constexpr (Z) {
+            const uint8_t* zu = z0 + at4;
 #pragma unroll
-            for (int i = 0; i < 2 * R; ++i)
-                lds_load16(cu + (co[i] + (Tail ? min(wk, left / 2 - 16) : wk)), t.w + 1024 * i);
-            const uint16_t* xu = x0 + k;
-#pragma unroll
-            for (int i = 0; i < 2 * NI; ++i)
-                lds_load16(xu + (xo[i] + (Tail ? min(xk[i], left - 8) : xk[i])), t.x + 1024 * i);
-            // scales two to a word, zero points four; a word past the last group repeats its word
-            const uint32_t first = unit * kGroups, at4 = first & ~3u;
-            const uint32_t end2 = ((groups - 1) & ~1u) - first, end4 = ((groups - 1) & ~3u) - at4;
-            const uint16_t* su = s0 + first;
-#pragma unroll
-            for (int i = 0; i < St::kSLoads; ++i) {
-                const uint32_t w = 2 * ((64 * i + lane) % kS);
-                lds_load4(su + (so[i] + (Tail ? min(w, end2) : w)), t.s + 64 * i);
+            for (int i = 0; i < St::kZLoads; ++i) {
+                const uint32_t w = 4 * ((64 * i + lane) % kZ);
+                lds_load4(zu + (zo[i] + (Tail ? min(w, end4) : w)), t.z + 64 * i);
             }
-            if constexpr (Z) {
-                const uint8_t* zu = z0 + at4;
-#pragma unroll
-                for (int i = 0; i < St::kZLoads; ++i) {
-                    const uint32_t w = 4 * ((64 * i + lane) % kZ);
-                    lds_load4(zu + (zo[i] + (Tail ? min(w, end4) : w)), t.z + 64 * i);
-                }
-            }
-        };
-        constexpr int kLoads = 2 * R + 2 * NI + St::kSLoads + St::kZLoads;
+        }
+    };
+    constexpr int kLoads = 2 * R + 2 * NI + St::kSLoads + St::kZLoads;
 
-        float sum[R][NI];
+    float sum[R][NI];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                sum[r][i] = 0.0f;
-        const auto compute = [&](int unit, int slot) {
-            const St& t = ring[wave][slot];
-            u32x4 q[R][2];
-            uint32_t sw[R][kS], zw[R][kZ];
+        for (int i = 0; i < NI; ++i)
+            sum[r][i] = 0.0f;
+    const auto compute = [&](int unit, int slot) {
+        const St& t = ring[wave][slot];
+        u32x4 q[R][2];
+        uint32_t sw[R][kS], zw[R][kZ];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = 16 * r + n16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q[r][h] = exchange(*reinterpret_cast<const u32x4*>(
+                    t.w + row * 128 + 16 * ((4 * h + g) ^ (row & 7))));
+#pragma unroll
+            for (int i = 0; i < kS; ++i)
+                sw[r][i] = t.s[row * kS + i];
+#pragma unroll
+            for (int i = 0; i < kZ; ++i)
+                zw[r][i] = Z ? t.z[row * kZ + i] : 0;
+        }
+        const int xr = (n16 >> 2) + 4 * ((n16 & 3) % NI);   // the token of operand row n16
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+            if (Tail && gr > 0 && unit * kUnit + gr * G >= p.K)
+                break;
+            f32x4 xs{}, acc[R] = {};
+#pragma unroll
+            for (int j = gr * kPer; j < (gr + 1) * kPer; ++j) {
+                const u32x4 x = in_order(*reinterpret_cast<const u32x4*>(
+                    t.x + xr * 512 + 16 * ((4 * j + g) ^ (xr & 7))));
+                xs = mma<F16>(x, ones, xs);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r] = mma<F16>(x, codes.operands(q[r][j >> 2][j & 3]), acc[r]);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int row = 16 * r + n16;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    q[r][h] = exchange(*reinterpret_cast<const u32x4*>(
-                        t.w + row * 128 + 16 * ((4 * h + g) ^ (row & 7))));
-#pragma unroll
-                for (int i = 0; i < kS; ++i)
-                    sw[r][i] = t.s[row * kS + i];
-#pragma unroll
-                for (int i = 0; i < kZ; ++i)
-                    zw[r][i] = Z ? t.z[row * kZ + i] : 0;
-            }
-            const int xr = (n16 >> 2) + 4 * ((n16 & 3) % NI);   // the token of operand row n16
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                if (Tail && gr > 0 && unit * kUnit + gr * G >= p.K)
-                    break;
-                f32x4 xs{}, acc[R] = {};
-#pragma unroll
-                for (int j = gr * kPer; j < (gr + 1) * kPer; ++j) {
-                    const u32x4 x = in_order(*reinterpret_cast<const u32x4*>(
-                        t.x + xr * 512 + 16 * ((4 * j + g) ^ (xr & 7))));
-                    xs = mma<F16>(x, ones, xs);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        acc[r] = mma<F16>(x, codes.operands(q[r][j >> 2][j & 3]), acc[r]);
+                const float scale = to_f32<F16>(sw[r][gr / 2] >> (16 * (gr & 1)));
+                float zero = 24.0f;
+                if constexpr (Z) {
+                    const int byte = G == 128 ? 2 * (unit & 1) + gr : gr & 3;
+                    zero = 16.0f + (float)((zw[r][G == 32 ? gr / 4 : 0] >> (8 * byte)) & 15u);
                 }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float scale = to_f32<F16>(sw[r][gr / 2] >> (16 * (gr & 1)));
-                    float zero = 24.0f;
-                    if constexpr (Z) {
-                        const int byte = G == 128 ? 2 * (unit & 1) + gr : gr & 3;
-                        zero = 16.0f + (float)((zw[r][G == 32 ? gr / 4 : 0] >> (8 * byte)) & 15u);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        sum[r][i] =
-                            __builtin_fmaf(scale, __builtin_fmaf(-zero, xs[i], acc[r][i]), sum[r][i]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    asm volatile("" : "+v"(sum[r][i]));     // see k_mv_i4
-        };
-
-        if (wave < p.units) {
-            const int last = p.units - 1;
-#pragma unroll
-            for (int d = 0; d < D - 1; ++d)
-                issue(min(wave + d * KW, last), d);
-            int slot = 0;
-            for (int unit = wave; unit < p.units; unit += KW) {
-                issue(min(unit + (D - 1) * KW, last), slot == 0 ? D - 1 : slot - 1);
-                // this unit has landed when only the D - 1 after it are outstanding
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kLoads) : "memory");
-                compute(unit, slot);
-                slot = slot == D - 1 ? 0 : slot + 1;
+                    sum[r][i] =
+                        __builtin_fmaf(scale, __builtin_fmaf(-zero, xs[i], acc[r][i]), sum[r][i]);
             }
         }
-        // this wave's ring holds its sums once the last loads have landed
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        float* red = reinterpret_cast<float*>(ring[wave]);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                red[(r * NI + i) * 64 + lane] = sum[r][i];
-        __syncthreads();
-        for (int u = wave; u < R * NI; u += KW) {
-            float v = 0.0f;
+                asm volatile("" : "+v"(sum[r][i]));     // see k_mv_i4
+    };
+
+    if (wave < p.units) {
+        const int last = p.units - 1;
 #pragma unroll
-            for (int w = 0; w < KW; ++w)
-                v += reinterpret_cast<const float*>(ring[w])[u * 64 + lane];
-            const int m = m0 + g + 4 * (u % NI), n = n0 + 16 * (u / NI) + n16;
-            if (m < p.rows && n < p.N)
-                p.y[m * p.ldy + n] = result<F16>(v);
+        for (int d = 0; d < D - 1; ++d)
+            issue(min(wave + d * KW, last), d);
+        int slot = 0;
+        for (int unit = wave; unit < p.units; unit += KW) {
+            issue(min(unit + (D - 1) * KW, last), slot == 0 ? D - 1 : slot - 1);
+            // this unit has landed when only the D - 1 after it are outstanding
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kLoads) : "memory");
+            compute(unit, slot);
+            slot = slot == D - 1 ? 0 : slot + 1;
         }
-        __syncthreads();
+    }
+    // this wave's ring holds its sums once the last loads have landed
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    float* red = reinterpret_cast<float*>(ring[wave]);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            red[(r * NI + i) * 64 + lane] = sum[r][i];
+    __syncthreads();
+    for (int u = wave; u < R * NI; u += KW) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+            v += reinterpret_cast<const float*>(ring[w])[u * 64 + lane];
+        const int m = g + 4 * (u % NI), n = n0 + 16 * (u / NI) + n16;
+        if (m < p.rows && n < p.N)
+            p.y[m * p.ldy + n] = result<F16>(v);
     }
 }
 
 template <bool F16, int G, bool Z, bool Tail, int NI, int R, int KW, int D>
-hipError_t launch_ms(const Args& a0, hipStream_t st) {
-    Args a = a0;
-    const int64_t chunks = ((int64_t)a.rows + 4 * NI - 1) / (4 * NI);
-    a.chunk = (int32_t)(chunks < 16384 ? chunks : 16384);
-    const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)), a.chunk);
+hipError_t launch_ms(const Args& a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R)));
     return launch1(k_ms_i4<F16, G, Z, Tail, NI, R, KW, D>, grid, dim3(64 * KW), st, a);
 }
 
 // The kernel for few rows.  Rules and measurements on MI355X (us):
-//  - Dense, up to 16 rows: k_ms_i4, in chunks of 4, 8 or 16 rows, with 32 rows of W for each
+//  - Dense, up to 16 rows: k_ms_i4, in forms for 4, 8 and 16 rows, with 32 rows of W for each
 //    workgroup (1 x 7168 x 7168, group 128: 8.2), or 16 where 32 would leave half of the compute
 //    units without one (1 x 1024 x 43008: 18.0 against 31.7; 16 x 1024 x 43008 27.4 against 38).
 //    Its lanes' offsets have 32 bits; where rows are so far apart that they do not fit, k_mv_i4.
@@ -1167,14 +1139,14 @@ template <bool F16, int G, bool Z, bool Tail>
 hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
     if (a.off) {
         if ((int64_t)a.experts * (a.N / 64) >= 512)
-            return launch_mv<F16, G, Z, Tail, 4, 1, 4, 4, 1>(a, st);
-        return launch_mv<F16, G, Z, Tail, 4, 1, 2, 4, 1>(a, st);
+            return launch_mv<F16, G, Z, Tail, 1, 4, 4>(a, st);
+        return launch_mv<F16, G, Z, Tail, 1, 2, 4>(a, st);
     }
     if (m <= 16) {
         const bool narrow = a.N < 4096;
         const auto near = [](int64_t rows, int64_t ld) { return ld < ((int64_t)1 << 31) / rows; };
         if (!near(32, a.ldc) || !near(32, a.lds) || !near(32, a.ldz) || !near(16, a.ldx))
-            return launch_mv<F16, G, Z, Tail, 4, 1, 2, 4, 1>(a, st);
+            return launch_mv<F16, G, Z, Tail, 1, 2, 4>(a, st);
         if (m <= 4)
             return narrow ? launch_ms<F16, G, Z, Tail, 1, 1, 8, 3>(a, st)
                           : launch_ms<F16, G, Z, Tail, 1, 2, 8, 2>(a, st);
@@ -1185,10 +1157,10 @@ hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
                       : launch_ms<F16, G, Z, Tail, 4, 2, 4, 2>(a, st);
     }
     if (((int64_t)a.N + 15) / 16 * ((m + 63) / 64) <= kComputeUnits)
-        return m <= 32 ? launch_mv<F16, G, Z, Tail, 4, 2, 1, 8, 1>(a, st)
-                       : launch_mv<F16, G, Z, Tail, 4, 4, 1, 8, 1>(a, st);
-    return m <= 32 ? launch_mv<F16, G, Z, Tail, 4, 2, 2, 4, 1>(a, st)
-                   : launch_mv<F16, G, Z, Tail, 4, 4, 2, 4, 1>(a, st);
+        return m <= 32 ? launch_mv<F16, G, Z, Tail, 2, 1, 8>(a, st)
+                       : launch_mv<F16, G, Z, Tail, 4, 1, 8>(a, st);
+    return m <= 32 ? launch_mv<F16, G, Z, Tail, 2, 2, 4>(a, st)
+                   : launch_mv<F16, G, Z, Tail, 4, 2, 4>(a, st);
 }
 
 // The kernel and tile for many rows (us, bf16, group 128, 8192 columns where no others are given):
