@@ -955,8 +955,15 @@ struct alignas(16) Staged {
     uint32_t z[Z ? 64 * kZLoads : 4];
 };
 
+// Waves on a SIMD that the rings leave room for: one where a workgroup of four waves takes more
+// than half of a compute unit's LDS (9 to 16 rows of x).
+template <int G, bool Z, int NI, int R, int KW, int D>
+constexpr int kStagedWaves =
+    160 * 1024 / (KW * D * (int)sizeof(Staged<G, Z, NI, R>)) * KW >= 8 ? 2 : 1;
+
 template <bool F16, int G, bool Z, bool Tail, int NI, int R, int KW, int D>
-__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) void k_ms_i4(Args p) {
+__global__ __launch_bounds__(64 * KW)
+__attribute__((amdgpu_waves_per_eu(kStagedWaves<G, Z, NI, R, KW, D>))) void k_ms_i4(Args p) {
     using St = Staged<G, Z, NI, R>;
     constexpr int kGroups = kUnit / G, kPer = 8 / kGroups;
     constexpr int kS = St::kS, kZ = St::kZ;
