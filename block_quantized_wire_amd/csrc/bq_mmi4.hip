@@ -319,9 +319,11 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
                                 scale, __builtin_fmaf(-zero, xs[t][i], acc[r][t][i]), sum[r][t][i]);
                 }
             }
-            // The sums stay in this block of instructions: the compiler has moved them behind the
-            // branch that follows, where a path reached them before the matrix instructions'
-            // results may be read (seen as wrong sums in binary16, group 128, one step of columns per wave).
+            // The sums are finished here, before the branch that follows.  Wrong sums were seen once
+            // without this, in a form of the kernel that was not kept (binary16, group 128, one
+            // unit a wave); the cause is not known.  It is no shortened wait in this file: with
+            // it or without, the compiler leaves 8 wait states or more on every path from a matrix
+            // instruction to a reader of its result.  It costs no time.
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -741,7 +743,7 @@ __global__ __launch_bounds__((64 * kTileWaves<TM, TN> * kTileParts<TN>), TM == 1
 #pragma unroll
         for (int i = 0; i < kSlots; ++i)
             fold(kSteps - 1, i);
-        // the sums stay in this block of instructions (see k_mv_i4)
+        // finished before the next branch (see k_mv_i4)
 #pragma unroll
         for (int m = 0; m < kMB; ++m)
 #pragma unroll
