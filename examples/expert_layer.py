@@ -164,6 +164,13 @@ def run(tokens=64, experts=16, topk=4, hidden=1024, inner=512, group=64, seed=0)
     return errors
 
 
+def close(errors: dict) -> bool:
+    """Whether the distances are those of roundings: less than one bf16 step for the layer, of
+    binary32 sums for the training step.  A NaN is not close."""
+    return all(errors[k] < 2.0 ** -8 for k in ("one token", "batch", "dropped")) and all(
+        errors[k] < 2.0 ** -12 for k in ("dx", "dweight"))
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, default in (("tokens", 64), ("experts", 16), ("topk", 4), ("hidden", 1024),
