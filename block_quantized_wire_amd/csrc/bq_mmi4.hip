@@ -380,11 +380,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(2))) vo
 //
 // 128 x 256, 4 waves, two workgroups to a compute unit.  Measured on MI355X (a large library
 // product reaches 1400 TFLOP/s): 24594 sorted rows over 32 experts of 2048 x 7168, group 64 with
-// zero points, 846 to 860 us in binary16 (840 to 854 TFLOP/s) and 1048 in bf16, whose zero points
-// cost a second multiply-add for each result; group 128 without 773 (934 TFLOP/s) and 917.
+// zero points, 832 to 861 us in binary16 (839 to 868 TFLOP/s) and 1042 in bf16, whose zero points
+// cost a second multiply-add for each result; group 128 without 776 (930 TFLOP/s) and 901.
 // What bounds it are the instructions between the matrix instructions: 264 vector and 64 matrix
 // instructions a stage and wave, of which 128 scale results and 88 make operands, with two
-// waves to a SIMD.  Scaling the operands instead of the results would save half of them and
+// waves to a SIMD.  By the counters the two kinds run one after the other: matrix cores busy 45% of
+// the cycles and vector instructions 51% in binary16, 33% and 54% in bf16.  Scaling the operands instead of the results would save half of them and
 // round every weight to 8 (11) bits, which it must not.  bf16's sums of x are made inside the
 // stage, with a barrier of their own: made a stage ahead they need a stage more in flight
 // (1146 against 917 us).  Registers are short: a spilled one is read back behind the stage's
@@ -942,10 +943,10 @@ hipError_t launch_mv(const Args& a, hipStream_t st) {
 // no barriers until the sums meet.  x has up to 4 NI rows (NI = 1, 2 or 4): a lane has NI results
 // for each block of 16 rows of W, result i of lane quarter g that of token g + 4i.
 // Measured at 16 x 7168 x 43008, group 64 with zero points (170 MB, 35 us at the rate of a large
-// copy): 57 us, against 76 with loads to registers.  Units of 128 columns, which leave room
+// copy): 56 us, against 74 with loads to registers.  Units of 128 columns, which leave room
 // for 8 waves, take 70 (runs of 64 bytes); pairs of waves that share a unit's x and meet at a
-// barrier for each 65; 16 rows of W 72, 64 rows 98.  Bound by the loads of x, 8 KB for 4 KB of
-// codes: one row of x takes 41 us (4.1 TB/s).
+// barrier for each 65; 16 rows of W 71, 64 rows 98.  Bound by the loads of x, 8 KB for 4 KB of
+// codes, with one wave to a SIMD: one row of x takes 41 to 44 us (3.9 to 4.1 TB/s).
 template <int G, bool Z, int NI, int R>
 struct alignas(16) Staged {
     static constexpr int kS = kUnit / G / 2;         // words of scales of a row and unit
@@ -1135,14 +1136,15 @@ hipError_t launch_ms(const Args& a, hipStream_t st) {
 
 // The kernel for few rows.  Rules and measurements on MI355X (us):
 //  - Dense, up to 16 rows: k_ms_i4, in forms for 4, 8 and 16 rows, with 32 rows of W for each
-//    workgroup (1 x 7168 x 7168, group 128: 8.2), or 16 where 32 would leave half of the compute
-//    units without one (1 x 1024 x 43008: 18.0 against 31.7; 16 x 1024 x 43008 27.4 against 38).
+//    workgroup (1 x 7168 x 7168, group 128: 7.3), or 16 where 32 would leave more than half of the
+//    compute units without one (1 x 1024 x 43008: 18.0 against 26; 16 x 1024 x 43008 27.6 against
+//    37).
 //    Its lanes' offsets have 32 bits; where rows are so far apart that they do not fit, k_mv_i4.
-//  - Above 16 rows k_mv_i4 with blocks of 16 tokens, two up to 32 rows (32 x 7168 x 7168: 19.9
-//    against 24.8 with four), else four; 16 rows of W to a workgroup of 8 waves instead of 32 to 4
+//  - Above 16 rows k_mv_i4 with blocks of 16 tokens, two up to 32 rows (32 x 7168 x 7168: 19.4
+//    against 25.6 with four), else four; 16 rows of W to a workgroup of 8 waves instead of 32 to 4
 //    where that still fits one round (64 x 1024 x 8192: 33 against 38, 24 rows 17 against 20).
 //  - By expert k_mv_i4 with four blocks of 16 rows of W to share the operands of x (8 rows for
-//    each of 64 experts of 4096 x 7168: 254 against 283 with two), or two where four leave
+//    each of 64 experts of 4096 x 7168: 243 against 280 with two), or two where four leave
 //    less than two workgroups to a compute unit.
 template <bool F16, int G, bool Z, bool Tail>
 hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
@@ -1174,16 +1176,18 @@ hipError_t launch_few(const Args& a, int64_t m, hipStream_t st) {
 
 // The kernel and tile for many rows (us, bf16, group 128, 8192 columns where no others are given):
 //  - k_mv_i4 while its workgroups, 64 rows of x by 32 of W, fit one round of a workgroup per
-//    compute unit: 64 x 8192 41 against 58 in tiles of 64 x 128, 64 x 16384 74 against 59.  Up to 32
-//    rows its rounds are shorter and three are taken (24 x 24576: 62 against 62), or six where such
-//    tiles would not fit one round (24 x 40960: 93 against 110; 24 x 57344: 126 against 115).
+//    compute unit: 64 x 8192 40 against 57 in tiles of 64 x 128, 64 x 16384 72 against 58.  Up to 32
+//    rows its rounds are shorter and three are taken (24 x 24576: 55 against 60), or six where such
+//    tiles would not fit one round (24 x 40960: 89 against 119; 24 x 57344: 123 against 115).
 //  - Tiles of 64 x 128, in two parts of the columns, while they fit one round: 256 x 7168 x 7168
-//    55 against 97 in tiles of 64 x 256; 512 x 7168 x 7168, 448 of them, 108 against 98.
-//  - Tiles of 128 x 256 where they make workgroups enough (7168 x 7168): 2048 rows 251 against
-//    297 in tiles of 64, 1024 rows 171 against 156; by expert 96 rows 680 against 663, 160 rows
-//    961 against 981.
-//  - By expert the tiles win from 16 rows an expert (64 experts of 4096 x 7168: 351 against 351
-//    there, 407 against 837 at 32).
+//    55 against 95 in tiles of 64 x 256; 512 x 7168 x 7168, 448 of them, 103 against 96.
+//  - Tiles of 128 x 256 where they make workgroups enough (7168 x 7168): 2048 rows 247 against
+//    290 in tiles of 64, 1024 rows 168 against 149; by expert 96 rows 688 against 651, 160 rows
+//    969 against 971.
+//  - By expert the tiles win from 16 rows an expert (64 experts of 4096 x 7168: 346 against 346
+//    there, 408 against 610 at 32).  The mean over the experts decides, since the host does not
+//    know their rows: 1024 rows that all go to one of the 64 stay with k_mv_i4, whose workgroups
+//    for that expert take them 16 at a time (1031; dealt evenly 337).
 template <bool F16, int G, bool Z>
 hipError_t launch_shape(const Args& a, hipStream_t st) {
     const int64_t m = a.off ? (a.rows + a.experts - 1) / a.experts : a.rows;
