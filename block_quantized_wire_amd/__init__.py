@@ -1,7 +1,8 @@
-"""libblockq: block-quantized wire codecs and an expert layer for AMD MI355X (gfx950).
+"""libblockq: block-quantized wire codecs, an expert layer and a 4-bit cache of keys and values
+with its attention, for AMD MI355X (gfx950).
 
-A thin ctypes binding over the C ABI declared in ``include/blockq.h`` and
-``include/blockq_moe.h``.  Every function here has the name of the C entry point
+A thin ctypes binding over the C ABI declared in ``include/blockq.h``,
+``include/blockq_moe.h`` and ``include/blockq_kv.h``.  Every function here has the name of the C entry point
 it calls and only marshals arguments: torch tensors give device pointers, the
 stream defaults to torch's current stream, and a non-OK status raises
 :class:`BlockqError`.  All compute runs in the HIP kernels of ``libblockq.so``;
@@ -39,6 +40,8 @@ __all__ = [
     "bq_moe_combine", "bq_moe_combine_f16", "bq_moe_combine_f32",
     "bq_moe_combine_bwd", "bq_moe_combine_bwd_f16", "bq_moe_combine_bwd_f32",
     "bq_moe_mm_i4", "bq_moe_mm_i4_f16",
+    "KvI4", "bq_kv_write_i4", "bq_kv_write_i4_f16", "bq_kv_read_i4", "bq_kv_read_i4_f16",
+    "bq_attn_i4", "bq_attn_i4_f16", "bq_attn_i4_ws_bytes",
     "bq_wire_bytes_b128", "bq_mm_tile_cols", "bq_status_str", "bq_version",
 ]
 
@@ -102,27 +105,31 @@ _SIGS = {
     "bq_moe_combine_bwd": [_P, _I64, _P, _I64, _P, _P, _P, _I64, _I, _I, _I64, _P, _I64, _P, _P],
     "bq_moe_mm_i4": [_P, _I64, _I64, _P, _I, _P, _I, _I64, _P, _I64, _I64, _P, _I64, _I64, _P,
                      _I64, _I64, _I64, _I64, _I, _P, _I64, _P],
+    "bq_kv_write_i4": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P],
+    "bq_kv_read_i4": [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P],
+    "bq_attn_i4": [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _I64,
+                   ctypes.c_float, _P, _I64, _I64, _P, _P, _I64, _P],
     "bq_quant_e4m3_b128": [_P, _I64, _P, _P, _P],
     "bq_dequant_e4m3_b128": [_P, _P, _I64, _P, _P],
 }
 for _name in ("bq_quant_i4", "bq_dequant_i4", "bq_mm_i4", "bq_moe_mm_i4", "bq_moe_combine",
-              "bq_moe_combine_bwd"):
+              "bq_moe_combine_bwd", "bq_kv_write_i4", "bq_kv_read_i4", "bq_attn_i4"):
     _SIGS[_name + "_f16"] = _SIGS[_name]
 for _name in ("bq_moe_combine", "bq_moe_combine_bwd"):
     _SIGS[_name + "_f32"] = _SIGS[_name]
 _lib = None
-_i32 = _f32 = None      # torch's types, known once the library is loaded
+_i32 = _f32 = _bf16 = _f16 = None      # torch's types, known once the library is loaded
 
 
 def _L() -> ctypes.CDLL:
     """The loaded libblockq.so (loaded on first use; a missing library is an error)."""
-    global _lib, _i32, _f32
+    global _lib, _i32, _f32, _bf16, _f16
     if _lib is None:
         # torch brings its own HIP runtime (same soname, libamdhip64.so.7).  Loading it
         # first makes libblockq.so bind to that one runtime; loaded the other way round,
         # the process would hold two HIP runtimes and ours would see no device.
         import torch
-        _i32, _f32 = torch.int32, torch.float32
+        _i32, _f32, _bf16, _f16 = torch.int32, torch.float32, torch.bfloat16, torch.float16
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python block_quantized_wire_amd/build.py` (hipcc, gfx950)")
@@ -137,6 +144,8 @@ def _L() -> ctypes.CDLL:
         L.bq_mx_scale_mfma_bytes.restype = _I64
         L.bq_moe_sort_ws_bytes.argtypes = [_I64, _I, _I]
         L.bq_moe_sort_ws_bytes.restype = _I64
+        L.bq_attn_i4_ws_bytes.argtypes = [_I64, _I64, _I64, _I64, _I, _I, _I]
+        L.bq_attn_i4_ws_bytes.restype = _I64
         L.bq_mm_tile_cols.argtypes = [_I64, _I64, ctypes.c_int]
         L.bq_mm_tile_cols.restype = ctypes.c_int
         L.bq_status_str.argtypes = [ctypes.c_int]
@@ -772,6 +781,187 @@ def bq_moe_mm_i4_f16(x, off, c, scale, y, zero=None, group: int = 128, src=None,
                      N: int | None = None, K: int | None = None, stream=None) -> None:
     """bq_moe_mm_i4 on IEEE binary16 x, scale and y."""
     _moe_mm_i4("bq_moe_mm_i4_f16", x, off, c, scale, y, zero, group, src, topk, N, K, stream)
+
+
+# ---- the 4-bit cache of keys and values, and attention over it ----------------------------
+#
+# slots, tables, lengths and starts: torch.int32, contiguous (a table's rows may be apart);
+# rows of keys, values, queries and results: (tokens, heads, dim) in the cache's type, the
+# last dimension contiguous, tokens and heads with any strides that the header allows.  Another
+# type is a TypeError, another shape, layout or device a ValueError.
+
+class _KvI4(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("ks", _P), ("vs", _P), ("page_stride", _I64),
+                ("head_stride", _I64), ("spage_stride", _I64), ("shead_stride", _I64),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class KvI4:
+    """A 4-bit cache of keys and values in the caller's tensors (the bq_kv_i4 of the C header).
+
+    k, v: torch.uint8 (pages, heads, page_size, dim / 2); ks, vs: torch.bfloat16 or torch.float16
+    (pages, heads, dim / group, page_size, 2).  What belongs to one page and head is contiguous;
+    pages and heads may lie anywhere, in the same way for k and v.  The tensors are kept
+    alive, and nothing of them is copied."""
+
+    def __init__(self, k, v, ks, vs, group: int = 128):
+        import torch
+        _L()
+        for arg, t, dtypes in (("k", k, (torch.uint8,)), ("v", v, (torch.uint8,)),
+                               ("ks", ks, (_bf16, _f16)), ("vs", vs, (ks.dtype,))):
+            if t.dtype not in dtypes:
+                raise TypeError(f"KvI4: {arg} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+        pages, heads, size, half = k.shape
+        dim = 2 * half
+        if group < 1 or dim % group or tuple(ks.shape) != (pages, heads, dim // group, size, 2):
+            raise ValueError(f"KvI4: ks has shape {tuple(ks.shape)} beside k's {tuple(k.shape)}")
+        for arg, a, b in (("v", v, k), ("vs", vs, ks)):
+            if a.shape != b.shape or a.stride() != b.stride() or a.device != k.device:
+                raise ValueError(f"KvI4: {arg} has another shape, layout or device than its partner")
+        if ks.device != k.device:
+            raise ValueError("KvI4: ks is on another device than k")
+        if size and (k.stride()[2:] != (half, 1) or ks.stride()[2:] != (2 * size, 2, 1)):
+            raise ValueError("KvI4: what belongs to one page and head is not contiguous")
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        self.pages, self.heads, self.page_size, self.dim, self.group = pages, heads, size, dim, group
+        self.dtype, self.device = ks.dtype, k.device
+        self.struct = _KvI4(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.stride(0),
+                            k.stride(1), ks.stride(0), ks.stride(1), pages, size, heads, dim, group)
+        self.address = ctypes.addressof(self.struct)
+
+
+def _refuse_rows(fn: str, cache, *arrays) -> None:
+    """Raise for the first of (name, rows, tokens, heads) that the cache does not go with, or for
+    a device other than the current one."""
+    for arg, t, tokens, heads in arrays:
+        if t.dtype is not cache.dtype:
+            raise TypeError(f"{fn}: {arg} is {t.dtype}, not the cache's {cache.dtype}")
+        if tuple(t.shape) != (tokens, heads, cache.dim):
+            raise ValueError(f"{fn}: {arg} is {tuple(t.shape)}, not {(tokens, heads, cache.dim)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{fn}: the last dimension of {arg} is not contiguous")
+        if t.device != cache.device:
+            raise ValueError(f"{fn}: {arg} is on {t.device}, the cache on {cache.device}")
+
+
+def _on_current(fn: str, cache, stream):
+    """The stream of a call, for a cache on torch's current device."""
+    stream = _stream(stream)
+    if cache.device.index != (_raw_device() if _raw_device else cache.device.index):
+        raise ValueError(f"{fn}: the cache is on {cache.device}, which is not the current device")
+    return stream
+
+
+def _kv_call(name, type_, k, v, slots, cache, stream, write):
+    lib, dtype = _L(), _f16 if type_ else _bf16
+    if cache.dtype is not dtype:
+        raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
+    tokens, heads = slots.numel(), cache.heads
+    shape = (tokens, heads, cache.dim)
+    if not (slots.dtype is _i32 and slots.is_contiguous()):
+        _refuse(name, ("slots", slots, _i32, 0))
+    ks, vs = k.stride(), v.stride()
+    if not (k.dtype is dtype and v.dtype is dtype and k.shape == shape and v.shape == shape
+            and ks[2] == 1 and vs[2] == 1 and k.device == v.device == slots.device == cache.device):
+        _refuse_rows(name, cache, ("k", k, tokens, heads), ("v", v, tokens, heads))
+        raise ValueError(f"{name}: slots is on {slots.device}, the cache on {cache.device}")
+    stream = _on_current(name, cache, stream)
+    rows = (k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
+    if write:
+        _check(name, getattr(lib, name)(*rows, slots.data_ptr(), tokens, cache.address, stream))
+    else:
+        _check(name, getattr(lib, name)(cache.address, slots.data_ptr(), tokens, *rows, stream))
+
+
+def bq_kv_write_i4(k, v, slots, cache, stream=None) -> None:
+    """k, v (tokens, heads, dim) torch.bfloat16 -> the cache's slots (tokens); a slot outside the
+    cache (-1) leaves its token out.  The slots of a call differ."""
+    _kv_call("bq_kv_write_i4", False, k, v, slots, cache, stream, True)
+
+
+def bq_kv_write_i4_f16(k, v, slots, cache, stream=None) -> None:
+    """bq_kv_write_i4 on IEEE binary16 rows and scales."""
+    _kv_call("bq_kv_write_i4_f16", True, k, v, slots, cache, stream, True)
+
+
+def bq_kv_read_i4(cache, slots, k, v, stream=None) -> None:
+    """The cache's slots (tokens) -> k, v (tokens, heads, dim) torch.bfloat16; zeros for a slot
+    outside the cache."""
+    _kv_call("bq_kv_read_i4", False, k, v, slots, cache, stream, False)
+
+
+def bq_kv_read_i4_f16(cache, slots, k, v, stream=None) -> None:
+    """bq_kv_read_i4 with IEEE binary16 scales and rows."""
+    _kv_call("bq_kv_read_i4_f16", True, k, v, slots, cache, stream, False)
+
+
+def bq_attn_i4_ws_bytes(seqs: int, rows: int, max_q: int, max_len: int, heads: int, kv_heads: int,
+                        dim: int) -> int:
+    """Scratch bytes of bq_attn_i4 (-1 for sizes outside its limits)."""
+    return _L().bq_attn_i4_ws_bytes(seqs, rows, max_q, max_len, heads, kv_heads, dim)
+
+
+def _attn_i4(name, type_, q, cache, table, lens, out, starts, max_q, max_len, causal, window, scale,
+             lse, ws, stream):
+    lib, i32, dtype = _L(), _i32, _f16 if type_ else _bf16
+    if cache.dtype is not dtype:
+        raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
+    shape, (seqs, cols), t_strides = q.shape, table.shape, table.stride()
+    rows, heads = shape[0], shape[1]
+    qs, os_ = q.stride(), out.stride()
+    if starts is None:
+        max_q = 1
+    elif max_q is None:
+        raise ValueError(f"{name}: max_q is needed beside starts")
+    if not (q.dtype is dtype and out.dtype is dtype and shape[2] == cache.dim and out.shape == shape
+            and qs[2] == 1 and os_[2] == 1 and table.dtype is i32 and lens.dtype is i32
+            and (t_strides[1] == 1 or cols < 2) and lens.is_contiguous() and lens.numel() == seqs
+            and (starts is None or starts.dtype is i32 and starts.is_contiguous()
+                 and starts.numel() == seqs + 1 and starts.device == cache.device)
+            and (lse is None or lse.dtype is _f32 and lse.is_contiguous()
+                 and lse.numel() == rows * heads and lse.device == cache.device)
+            and (ws is None or ws.is_contiguous() and ws.device == cache.device)
+            and q.device == out.device == table.device == lens.device == cache.device):
+        _refuse_rows(name, cache, ("q", q, rows, heads), ("out", out, rows, heads))
+        _refuse(name, ("lens", lens, i32, seqs), ("starts", 0 if starts is None else starts, i32, seqs + 1),
+                ("lse", 0 if lse is None else lse, _f32, rows * heads))
+        if table.dtype is not i32:
+            raise TypeError(f"{name}: table is {table.dtype}, not {i32}")
+        raise ValueError(f"{name}: table, lens, starts, lse or ws has another length, layout or device "
+                         f"than q {tuple(shape)} and table {(seqs, cols)} ask for")
+    if scale is None:
+        scale = cache.dim ** -0.5
+    stream = _on_current(name, cache, stream)
+    _check(name, getattr(lib, name)(
+        q.data_ptr(), qs[0], qs[1], cache.address, table.data_ptr(), t_strides[0] if seqs > 1 else cols,
+        cols, lens.data_ptr(), None if starts is None else starts.data_ptr(), seqs, rows, max_q,
+        cols * cache.page_size if max_len is None else max_len, heads, causal, window, scale,
+        out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), stream))
+
+
+def bq_attn_i4(q, cache, table, lens, out, starts=None, max_q: int | None = None,
+               max_len: int | None = None, causal: bool = True, window: int = 0,
+               scale: float | None = None, lse=None, ws=None, stream=None) -> None:
+    """Attention of q (rows, heads, dim) torch.bfloat16 over the cache -> out, and lse (rows, heads)
+    torch.float32 where given.
+
+    table (seqs, pages of a sequence), lens (seqs): each sequence's pages and tokens in the cache.
+    starts (seqs + 1): rows [starts[b], starts[b+1]) of q are sequence b's last tokens, at most
+    max_q of them; None: row b alone.  max_len: at least every length (None: all that a row of the
+    table has room for).  window: a row sees that many tokens at most, 0 all.  scale: dim ** -0.5
+    where left out.  ws: scratch of at least bq_attn_i4_ws_bytes bytes, or None where that is 0."""
+    _attn_i4("bq_attn_i4", False, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
+             scale, lse, ws, stream)
+
+
+def bq_attn_i4_f16(q, cache, table, lens, out, starts=None, max_q: int | None = None,
+                   max_len: int | None = None, causal: bool = True, window: int = 0,
+                   scale: float | None = None, lse=None, ws=None, stream=None) -> None:
+    """bq_attn_i4 on IEEE binary16 q, scales and out."""
+    _attn_i4("bq_attn_i4_f16", True, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
+             scale, lse, ws, stream)
 
 
 # ---- E4M3 128-block codec ------------------------------------------------------------------

@@ -7,14 +7,17 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libblockq.so")
 SOURCES = ["bq_abi.cpp", "bq_i8.hip", "bq_mx.hip", "bq_mxc.hip", "bq_mm.hip", "bq_noalloc.hip",
-           "bq_i4.hip", "bq_mmi4.hip", "bq_moe.hip"]
-HEADERS = ["bq_device.h", "bq_launch.h", "bq_ranges.h"]
+           "bq_i4.hip", "bq_mmi4.hip", "bq_moe.hip", "bq_kv.hip", "bq_attn.hip", "bq_attn_64.hip",
+           "bq_attn_256.hip"]
+HEADERS = ["bq_device.h", "bq_launch.h", "bq_ranges.h", "bq_attn.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -22,7 +25,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # the codec definitions round every product and sum separately, in IEEE binary32
     "-ffp-contract=off",
     "-fno-fast-math",
@@ -41,10 +43,17 @@ def sources() -> list[str]:
 def build(verbose: bool = False) -> str:
     """Compile every HIP source for gfx950 into block_quantized_wire_amd/libblockq.so."""
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    include = ["-I", os.path.join(ROOT, "include")]
+    with tempfile.TemporaryDirectory() as d:
+        # the sources side by side: the attention's alone take a minute each
+        cmds = [[HIPCC, *FLAGS, *include, "-c", s, "-o", os.path.join(d, os.path.basename(s) + ".o")]
+                for s in sources()]
+        if verbose:
+            print("\n".join(" ".join(c) for c in cmds), flush=True)
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
+        subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *(c[-1] for c in cmds), "-o", tmp],
+                       check=True)
     os.replace(tmp, LIB)
     return LIB
 
@@ -54,7 +63,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(ROOT, "include", h) for h in ("blockq.h", "blockq_moe.h")]
+        os.path.join(ROOT, "include", h) for h in ("blockq.h", "blockq_moe.h", "blockq_kv.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -6,6 +6,7 @@
 // Compatibility).  The library allocates nothing, keeps no state and never
 // synchronizes, so every call may be captured in a HIP graph.
 #include "blockq.h"
+#include "blockq_kv.h"
 #include "blockq_moe.h"
 
 #include <hip/hip_runtime.h>
@@ -1289,6 +1290,299 @@ bq_status bq_moe_mm_i4_f16(const uint16_t* x, int64_t ldx, int64_t x_rows, const
                            int64_t ldy, void* stream) {
     return moe_mm_i4(x, ldx, x_rows, src, topk, off, experts, rows, c, ldc, stride_c, scale, lds,
                      stride_s, zero, ldz, stride_z, N, K, group, y, ldy, true, stream);
+}
+
+// ---- the 4-bit cache of keys and values ------------------------------------------------------
+
+namespace {
+
+constexpr int kMaxKvHeads = 1024;
+constexpr int kMaxShare = 64;                       // heads of q to a head of the cache
+constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+constexpr int64_t kMaxLen = (int64_t)1 << 30;
+
+// Bytes from the first to the last of `n` x `m` pieces of `size`, `sn` and `sm` apart.
+int64_t nest_bytes(int64_t n, int64_t sn, int64_t m, int64_t sm, int64_t size) {
+    return (n - 1) * sn + (m - 1) * sm + size;
+}
+
+// Whether those pieces lie within the largest operand; apart: and none overlaps another, one of
+// the two nested in the other.
+bool nest_fits(int64_t n, int64_t sn, int64_t m, int64_t sm, int64_t size, bool apart) {
+    const int64_t most = kMaxExtentBytes;
+    if (sn < 0 || sm < 0 || (n > 1 && sn > most / (n - 1)) || (m > 1 && sm > most / (m - 1)) ||
+        nest_bytes(n, sn, m, sm, size) > most)
+        return false;
+    if (!apart)
+        return true;
+    const bool n_outer = (m == 1 || sm >= size) && (n == 1 || sn >= (m - 1) * sm + size);
+    const bool m_outer = (n == 1 || sn >= size) && (m == 1 || sm >= (n - 1) * sn + size);
+    return n_outer || m_outer;
+}
+
+bool width_ok(int dim) { return dim == 64 || dim == 128 || dim == 256; }
+
+bq_status check_kv(const bq_kv_i4* c) {
+    if (!c)
+        return BQ_ERR_NULL;
+    if (!width_ok(c->dim) || !group_ok(c->group) || c->group > c->dim || c->heads < 1 ||
+        c->heads > kMaxKvHeads || c->pages < 1 || c->page_size < 8 || c->page_size % 8 != 0 ||
+        (int64_t)c->pages * c->page_size >= (int64_t)1 << 31)
+        return BQ_ERR_SIZE;
+    return BQ_OK;
+}
+
+int64_t kv_code_bytes(const bq_kv_i4& c) { return (int64_t)c.page_size * (c.dim / 2); }
+int64_t kv_scale_bytes(const bq_kv_i4& c) { return (int64_t)c.page_size * (c.dim / c.group) * 4; }
+
+// The pool's arrays; spans of k, v, ks, vs.
+bq_status check_kv_arrays(const bq_kv_i4& c, Span s[4]) {
+    if (!c.k || !c.v || !c.ks || !c.vs)
+        return BQ_ERR_NULL;
+    if (c.spage_stride > kMaxExtentBytes || c.shead_stride > kMaxExtentBytes)
+        return BQ_ERR_BOUNDS;
+    const int64_t codes = kv_code_bytes(c), scales = kv_scale_bytes(c);
+    if (!nest_fits(c.pages, c.page_stride, c.heads, c.head_stride, codes, true) ||
+        !nest_fits(c.pages, 2 * c.spage_stride, c.heads, 2 * c.shead_stride, scales, true))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.ks, 16) || !aligned(c.vs, 16) ||
+        c.page_stride % 16 != 0 || c.head_stride % 16 != 0 || c.spage_stride % 8 != 0 ||
+        c.shead_stride % 8 != 0)
+        return BQ_ERR_ALIGN;
+    const int64_t cb = nest_bytes(c.pages, c.page_stride, c.heads, c.head_stride, codes);
+    const int64_t sb = nest_bytes(c.pages, 2 * c.spage_stride, c.heads, 2 * c.shead_stride, scales);
+    s[0] = span(c.k, cb);
+    s[1] = span(c.v, cb);
+    s[2] = span(c.ks, sb);
+    s[3] = span(c.vs, sb);
+    return BQ_OK;
+}
+
+// Rows [n][heads][dim] of 16-bit numbers with a row and a head stride in entries.
+bq_status check_rows(const void* x, int64_t n, int64_t ld, int64_t heads, int64_t hs, int64_t dim,
+                     bool apart) {
+    if (!x)
+        return BQ_ERR_NULL;
+    if (ld < 0 || hs < 0 || ld > kMaxExtentBytes || hs > kMaxExtentBytes ||
+        !nest_fits(n, 2 * ld, heads, 2 * hs, 2 * dim, apart))
+        return BQ_ERR_BOUNDS;
+    return aligned(x, 16) && ld % 8 == 0 && hs % 8 == 0 ? BQ_OK : BQ_ERR_ALIGN;
+}
+Span rows_span(const void* x, int64_t n, int64_t ld, int64_t heads, int64_t hs, int64_t dim) {
+    return span(x, nest_bytes(n, 2 * ld, heads, 2 * hs, 2 * dim));
+}
+
+// The pool's k, v, ks and vs may share one allocation, page by page, so their spans may interleave:
+// only pieces of the same address are refused.
+bool kv_arrays_same(const bq_kv_i4& c) {
+    const void* p[4] = {c.k, c.v, c.ks, c.vs};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (p[i] == p[j])
+                return true;
+    return false;
+}
+
+bq_status check_slots(const int32_t* slot, int64_t tokens, const bq_kv_i4* cache) {
+    BQ_TRY(check_kv(cache));
+    if (tokens < 0 || tokens >= ((int64_t)1 << 31) / cache->heads)
+        return BQ_ERR_SIZE;
+    if (tokens == 0)
+        return BQ_OK;
+    if (!slot)
+        return BQ_ERR_NULL;
+    return aligned(slot, 4) ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+bq_status kv_write(const uint16_t* k, int64_t ldk, int64_t hsk, const uint16_t* v, int64_t ldv,
+                   int64_t hsv, const int32_t* slot, int64_t tokens, const bq_kv_i4* cache, bool f16,
+                   void* stream) {
+    BQ_TRY(check_slots(slot, tokens, cache));
+    if (tokens == 0)
+        return BQ_OK;
+    const bq_kv_i4& c = *cache;
+    Span outs[4];
+    BQ_TRY(check_kv_arrays(c, outs));
+    BQ_TRY(check_rows(k, tokens, ldk, c.heads, hsk, c.dim, false));
+    BQ_TRY(check_rows(v, tokens, ldv, c.heads, hsv, c.dim, false));
+    const Span ins[3] = {rows_span(k, tokens, ldk, c.heads, hsk, c.dim),
+                         rows_span(v, tokens, ldv, c.heads, hsv, c.dim), span(slot, 4 * tokens)};
+    if (kv_arrays_same(c))
+        return BQ_ERR_ALIAS;
+    for (const Span& o : outs)
+        for (const Span& i : ins)
+            if (overlaps(o, i))
+                return BQ_ERR_ALIAS;
+    bq::KvRows r{};
+    r.k = k;
+    r.v = v;
+    r.ldk = ldk;
+    r.hsk = hsk;
+    r.ldv = ldv;
+    r.hsv = hsv;
+    r.slot = slot;
+    r.tokens = tokens;
+    return launched(bq::launch_kv_write(r, c, f16, as_stream(stream)));
+}
+
+bq_status kv_read(const bq_kv_i4* cache, const int32_t* slot, int64_t tokens, uint16_t* k,
+                  int64_t ldk, int64_t hsk, uint16_t* v, int64_t ldv, int64_t hsv, bool f16,
+                  void* stream) {
+    BQ_TRY(check_slots(slot, tokens, cache));
+    if (tokens == 0)
+        return BQ_OK;
+    const bq_kv_i4& c = *cache;
+    Span ins[5];
+    BQ_TRY(check_kv_arrays(c, ins));
+    BQ_TRY(check_rows(k, tokens, ldk, c.heads, hsk, c.dim, true));
+    BQ_TRY(check_rows(v, tokens, ldv, c.heads, hsv, c.dim, true));
+    ins[4] = span(slot, 4 * tokens);
+    const Span outs[2] = {rows_span(k, tokens, ldk, c.heads, hsk, c.dim),
+                          rows_span(v, tokens, ldv, c.heads, hsv, c.dim)};
+    // k and v may be parts of the same rows: their spans interleave then
+    if (k == v || any_overlap(outs, 1, ins, 5) || any_overlap(outs + 1, 1, ins, 5))
+        return BQ_ERR_ALIAS;
+    bq::KvRows r{};
+    r.ko = k;
+    r.vo = v;
+    r.ldk = ldk;
+    r.hsk = hsk;
+    r.ldv = ldv;
+    r.hsv = hsv;
+    r.slot = slot;
+    r.tokens = tokens;
+    return launched(bq::launch_kv_read(r, c, f16, as_stream(stream)));
+}
+
+bq_status check_attn_sizes(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
+                           int kv_heads) {
+    if (seqs < 0 || seqs > kMaxSeqs || rows < 0 || max_q < 0 || max_q > kMaxSeqs || max_len < 0 ||
+        max_len >= kMaxLen || kv_heads < 1 || kv_heads > kMaxKvHeads || heads < 1 ||
+        heads % kv_heads != 0 || heads / kv_heads > kMaxShare)
+        return BQ_ERR_SIZE;
+    if (rows >= ((int64_t)1 << 31) / heads)
+        return BQ_ERR_SIZE;
+    return BQ_OK;
+}
+
+bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* cache,
+                  const int32_t* table, int64_t ldt, int64_t table_cols, const int32_t* lens,
+                  const int32_t* starts, int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len,
+                  int heads, int causal, int64_t window, float scale, uint16_t* out, int64_t ldo,
+                  int64_t hso, float* lse, void* ws, int64_t ws_bytes, bool f16, void* stream) {
+    BQ_TRY(check_kv(cache));
+    const bq_kv_i4& c = *cache;
+    BQ_TRY(check_attn_sizes(seqs, rows, max_q, max_len, heads, c.heads));
+    if (table_cols < 0 || table_cols > kMaxLen || window < 0)
+        return BQ_ERR_SIZE;
+    if (seqs == 0 || rows == 0 || max_q == 0)
+        return BQ_OK;
+    if (!table || !lens)
+        return BQ_ERR_NULL;
+    Span ins[8];
+    BQ_TRY(check_kv_arrays(c, ins));
+    BQ_TRY(check_rows(q, rows, ldq, heads, hsq, c.dim, false));
+    BQ_TRY(check_rows(out, rows, ldo, heads, hso, c.dim, true));
+    if (ldt < table_cols || !extent_fits(seqs, table_cols, ldt, 4))
+        return BQ_ERR_BOUNDS;
+    if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(lse, 4))
+        return BQ_ERR_ALIGN;
+    const bq::AttnPlan plan =
+        bq::attn_plan(seqs, rows, starts ? max_q : 1, max_len, heads, c.heads, c.dim);
+    if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes))
+        return BQ_ERR_SCRATCH;
+    if (plan.ws_bytes > 0 && !aligned(ws, 16))
+        return BQ_ERR_ALIGN;
+    if (seqs * c.heads * plan.tiles * plan.splits >= (int64_t)1 << 24 ||
+        seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 26)
+        return BQ_ERR_SIZE;
+    ins[4] = rows_span(q, rows, ldq, heads, hsq, c.dim);
+    ins[5] = span(table, extent(seqs, table_cols, ldt, 4));
+    ins[6] = span(lens, 4 * seqs);
+    ins[7] = span(starts, starts ? 4 * (seqs + 1) : 0);
+    const Span outs[3] = {rows_span(out, rows, ldo, heads, hso, c.dim),
+                          span(lse, lse ? 4 * rows * heads : 0), span(ws, plan.ws_bytes)};
+    if (any_overlap(outs, 3, ins, 8))
+        return BQ_ERR_ALIAS;
+    bq::AttnI4 a{};
+    a.q = q;
+    a.c = c;
+    a.table = table;
+    a.lens = lens;
+    a.starts = starts;
+    a.out = out;
+    a.lse = lse;
+    a.ws = ws;
+    a.ldq = ldq;
+    a.hsq = hsq;
+    a.ldo = ldo;
+    a.hso = hso;
+    a.ldt = ldt;
+    a.table_cols = (int32_t)table_cols;
+    a.seqs = (int32_t)seqs;
+    a.rows = (int32_t)rows;
+    a.max_q = (int32_t)(starts ? max_q : 1);
+    a.max_len = (int32_t)max_len;
+    a.heads = heads;
+    a.causal = causal != 0;
+    a.window = (int32_t)(window < kMaxLen ? window : kMaxLen);
+    a.scale = scale;
+    return launched(bq::launch_attn_i4(a, plan, f16, as_stream(stream)));
+}
+
+}  // namespace
+
+bq_status bq_kv_write_i4(const uint16_t* k, int64_t ldk, int64_t hsk, const uint16_t* v, int64_t ldv,
+                         int64_t hsv, const int32_t* slot, int64_t tokens, const bq_kv_i4* cache,
+                         void* stream) {
+    return kv_write(k, ldk, hsk, v, ldv, hsv, slot, tokens, cache, false, stream);
+}
+
+bq_status bq_kv_read_i4(const bq_kv_i4* cache, const int32_t* slot, int64_t tokens, uint16_t* k,
+                        int64_t ldk, int64_t hsk, uint16_t* v, int64_t ldv, int64_t hsv,
+                        void* stream) {
+    return kv_read(cache, slot, tokens, k, ldk, hsk, v, ldv, hsv, false, stream);
+}
+
+bq_status bq_attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* cache,
+                     const int32_t* table, int64_t ldt, int64_t table_cols, const int32_t* lens,
+                     const int32_t* starts, int64_t seqs, int64_t rows, int64_t max_q,
+                     int64_t max_len, int heads, int causal, int64_t window, float scale,
+                     uint16_t* out, int64_t ldo, int64_t hso, float* lse, void* ws,
+                     int64_t ws_bytes, void* stream) {
+    return attn_i4(q, ldq, hsq, cache, table, ldt, table_cols, lens, starts, seqs, rows, max_q,
+                   max_len, heads, causal, window, scale, out, ldo, hso, lse, ws, ws_bytes, false, stream);
+}
+
+bq_status bq_kv_write_i4_f16(const uint16_t* k, int64_t ldk, int64_t hsk, const uint16_t* v, int64_t ldv,
+                         int64_t hsv, const int32_t* slot, int64_t tokens, const bq_kv_i4* cache,
+                         void* stream) {
+    return kv_write(k, ldk, hsk, v, ldv, hsv, slot, tokens, cache, true, stream);
+}
+
+bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t tokens, uint16_t* k,
+                        int64_t ldk, int64_t hsk, uint16_t* v, int64_t ldv, int64_t hsv,
+                        void* stream) {
+    return kv_read(cache, slot, tokens, k, ldk, hsk, v, ldv, hsv, true, stream);
+}
+
+bq_status bq_attn_i4_f16(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* cache,
+                     const int32_t* table, int64_t ldt, int64_t table_cols, const int32_t* lens,
+                     const int32_t* starts, int64_t seqs, int64_t rows, int64_t max_q,
+                     int64_t max_len, int heads, int causal, int64_t window, float scale,
+                     uint16_t* out, int64_t ldo, int64_t hso, float* lse, void* ws,
+                     int64_t ws_bytes, void* stream) {
+    return attn_i4(q, ldq, hsq, cache, table, ldt, table_cols, lens, starts, seqs, rows, max_q,
+                   max_len, heads, causal, window, scale, out, ldo, hso, lse, ws, ws_bytes, true, stream);
+}
+
+int64_t bq_attn_i4_ws_bytes(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
+                            int kv_heads, int dim) {
+    if (!width_ok(dim) || check_attn_sizes(seqs, rows, max_q, max_len, heads, kv_heads) != BQ_OK)
+        return -1;
+    if (seqs == 0 || rows == 0 || max_q == 0)
+        return 0;
+    return bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim).ws_bytes;
 }
 
 // ---- E4M3 128-block codec ------------------------------------------------------------------

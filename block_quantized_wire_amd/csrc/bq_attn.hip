@@ -1,0 +1,54 @@
+// bq_attn.hip -- attention over the 4-bit cache: how a call is cut, and heads of 128 numbers.
+#include "bq_attn.h"
+
+namespace bq {
+
+namespace attn {
+
+hipError_t launch_width(std::integral_constant<int, 128>, const Args& a, const AttnPlan& p, bool f16,
+                        hipStream_t stream) {
+    return launch_any<128>(a, p, f16, stream);
+}
+
+}  // namespace attn
+
+AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
+                   int kv_heads, int dim) {
+    AttnPlan p{};
+    const int64_t m = max_q * (heads / kv_heads);       // rows of one sequence and cache head
+    p.by_rows = m > 32;
+    p.cols = m <= 16 || (p.by_rows && m <= 64) ? 1 : m <= 128 || dim == 256 ? 2 : 4;
+    const int64_t tile = 16 * p.cols * (p.by_rows ? attn::kWaves : 1);
+    p.tiles = (int)((m + tile - 1) / tile);
+    const int64_t base = seqs * kv_heads * p.tiles;
+    // four workgroups to a compute unit, and 256 tokens or more to a workgroup
+    int64_t splits = 1024 / (base > 0 ? base : 1);
+    const int64_t longest = (max_len + 255) / 256;
+    splits = splits < longest ? splits : longest;
+    const int64_t cell = rows * heads * 4 * (dim + 2);
+    const int64_t room = ((int64_t)64 << 20) / (cell > 0 ? cell : 1);
+    splits = splits < room ? splits : room;
+    p.splits = (int)(splits < 1 ? 1 : splits);
+    p.ws_bytes = p.splits > 1 ? p.splits * cell : 0;
+    return p;
+}
+
+hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStream_t stream) {
+    attn::Args g{};
+    g.a = a;
+    g.units = (int32_t)((int64_t)a.seqs * a.c.heads * p.splits);
+    g.tiles = p.tiles;
+    g.splits = p.splits;
+    g.share = a.heads / a.c.heads;
+    g.bpp = a.c.page_size / 8;
+    g.scale2 = a.scale * 1.44269504088896341f;
+    if (p.splits > 1) {
+        g.part = static_cast<float*>(a.ws);
+        g.ml = g.part + (int64_t)p.splits * a.rows * a.heads * a.c.dim;
+    }
+    return a.c.dim == 64    ? attn::launch_width(std::integral_constant<int, 64>{}, g, p, f16, stream)
+           : a.c.dim == 128 ? attn::launch_width(std::integral_constant<int, 128>{}, g, p, f16, stream)
+                            : attn::launch_width(std::integral_constant<int, 256>{}, g, p, f16, stream);
+}
+
+}  // namespace bq

@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "blockq_kv.h"
+
 namespace bq {
 
 // Launch `kernel` with its one by-value argument struct on `stream` and return the
@@ -146,5 +148,43 @@ hipError_t launch_moe_combine(const MoeRows& r, MoeType type, const void* rows, 
 hipError_t launch_moe_combine_bwd(const MoeRows& r, MoeType type, const void* dy, int64_t lddy,
                                   const void* rows, int64_t ldr, const float* weight, void* drows,
                                   int64_t lddr, float* dweight, hipStream_t stream);
+
+// The 4-bit cache of keys and values (see include/blockq_kv.h for the layouts).
+struct KvRows {
+    const uint16_t *k, *v;     // rows read by a write
+    uint16_t *ko, *vo;         // rows written by a read
+    int64_t ldk, hsk, ldv, hsv;
+    const int32_t* slot;
+    int64_t tokens;
+};
+hipError_t launch_kv_write(const KvRows& r, const bq_kv_i4& c, bool f16, hipStream_t stream);
+hipError_t launch_kv_read(const KvRows& r, const bq_kv_i4& c, bool f16, hipStream_t stream);
+
+struct AttnI4 {
+    const uint16_t* q;
+    bq_kv_i4 c;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* starts;
+    uint16_t* out;
+    float* lse;
+    void* ws;
+    int64_t ldq, hsq, ldo, hso, ldt;
+    int32_t table_cols, seqs, rows, max_q, max_len, heads;
+    int32_t causal, window;
+    float scale;
+};
+// How a call is cut: `cols` rows (of one key-value head: tokens times the heads that share it)
+// to a tile, and the tokens of a sequence over `splits` workgroups, whose partial results the
+// workspace holds.
+struct AttnPlan {
+    bool by_rows;      // waves of a workgroup take rows of their own, not tokens
+    int cols;          // blocks of 16 rows to a wave
+    int tiles, splits;
+    int64_t ws_bytes;
+};
+AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
+                   int kv_heads, int dim);
+hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStream_t stream);
 
 }  // namespace bq
