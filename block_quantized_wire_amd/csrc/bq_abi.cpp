@@ -1494,7 +1494,7 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
     if (plan.ws_bytes > 0 && !aligned(ws, 16))
         return BQ_ERR_ALIGN;
     if (seqs * c.heads * plan.tiles * plan.splits >= (int64_t)1 << 24 ||
-        seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 26)
+        (plan.splits > 1 && seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 24))
         return BQ_ERR_SIZE;
     ins[4] = rows_span(q, rows, ldq, heads, hsq, c.dim);
     ins[5] = span(table, extent(seqs, table_cols, ldt, 4));

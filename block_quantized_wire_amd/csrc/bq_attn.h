@@ -12,10 +12,10 @@
 // cores take exactly.  A word of 8 codes becomes 4 registers of 2 operands with 4 ANDs and a
 // shift.  q is scaled by a power of two to just below 2^14 (its numbers that meet the codes four
 // bits higher by 2^-4 more), so binary16 holds it exactly but for numbers 2^-24 below the largest.
-// Codes of values are centred to c - 8 first, an instruction more for two: over many tokens the
-// result is small beside the sums of c s and of m, and would be lost in their binary32 rounding.
-// p_t s_tg goes in as one binary16 number where the result is bf16, whose rounding is 8 times as
-// large; for binary16 results as a sum of two (22 bits in all).
+// Codes of values are centred to c - 8: over many tokens the result is small beside the sums of c s
+// and of m, and would be lost in their binary32 rounding.
+// p goes in as one binary16 number where the result is bf16, whose rounding is 8 times as large;
+// for binary16 results as a sum of two (22 bits in all).
 //
 // Steps.  A wave takes 32 tokens a step, as the rows of two 16x16x32 products with 16 * NC rows of
 // q (rows of one cache head: tokens times the heads that share it).  Row 4b + i of the two is
@@ -25,9 +25,8 @@
 // one run of dim/8 and one of dim/4 bytes.
 //
 // Softmax: R, the reference of a row, is only raised when a score passes it by 8 (a
-// factor of 2^8), which a wave tests once a step.  p is 2^k times as large as written above, with
-// a k of the wave that brings the largest scale of values to just below 2^7: p s then fills the
-// range of binary16.  2^k is in the row's sums of p too, and leaves with the division.
+// factor of 2^8), which a wave tests once a step; the same branch keeps the power of two that
+// brings the values' sizes into the range of binary16.
 #pragma once
 
 #include <type_traits>
@@ -45,12 +44,32 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kStep = 32;           // tokens of a step
+constexpr int kMaxSplits = 256;     // of the tokens of a sequence
 constexpr float kRaise = 8.0f;      // a score may pass R by this, in powers of two
+
+// Division of n < 2^27 by a d known to the host: with 2^(p - 27) >= d and mul = ceil(2^p / d),
+// n * mul passes n * 2^p / d by less than 2^p / d, which no quotient notices.
+struct Div {
+    uint32_t d, mul, p;
+    static Div by(uint32_t d) {
+        uint32_t p = 27;
+        while (((uint64_t)1 << (p - 27)) < d)
+            ++p;
+        return Div{d, (uint32_t)((((uint64_t)1 << p) + d - 1) / d), p};
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return (int)((uint64_t)(uint32_t)n * mul >> p);
+    }
+    __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+};
 
 struct Args {
     AttnI4 a;
-    int32_t units;      // seqs * cache heads * splits
-    int32_t tiles, splits, share, bpp;
+    Div units;          // seqs * cache heads * splits
+    Div heads, by_splits;
+    Div share;          // heads of q to one of the cache
+    Div bpp;            // blocks of 8 tokens to a page
+    int32_t tiles, splits;
     float scale2;       // scale * log2(e)
     float* part;        // partial results [splits][rows][heads][D], relative to their R
     float* ml;          // [splits][rows][heads][2]: R, sum of p
@@ -61,7 +80,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // The value of lane `Lane` of each row of 16 lanes.
 template <int Lane>
 __device__ __forceinline__ float bcast(float v) {
-    return __uint_as_float(dpp<0x150 + Lane>(__float_as_uint(v)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x150 + Lane, 0xF,
+                                                              0xF, true));
 }
 
 template <bool F16>
@@ -124,13 +144,40 @@ __device__ __forceinline__ h16x8 codes8(uint32_t w) {
         h16x8, u32x4{w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u});
 }
 
-// Codes c of the low (high: of the next four) bits of both half-words as c - 8 (16 times that):
-// 1024 + c is a binary16 number with c in its low bits.
-__device__ __forceinline__ uint32_t centred(uint32_t w, bool high) {
-    const uint32_t m = high ? 0x00F000F0u : 0x000F000Fu;
-    const h16x2 off = high ? h16x2{(_Float16)-1152.0f, (_Float16)-1152.0f}
-                           : h16x2{(_Float16)-1032.0f, (_Float16)-1032.0f};
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, (w & m) | 0x64006400u) + off);
+// Codes c of the low bits of both half-words as c - 8: 1024 + c is a binary16 number with c in its
+// low bits.  v_and_or_b32 takes one constant that is not in a vector register.
+__device__ __forceinline__ uint32_t centred(uint32_t w) {
+    uint32_t one = 0x64006400u;
+    asm("" : "+v"(one));
+    const h16x2 off{(_Float16)-1032.0f, (_Float16)-1032.0f};
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, (w & 0x000F000Fu) | one) + off);
+}
+
+// Global-to-LDS load of 16 (4) bytes per lane: lane i's land at lds + 16 i (4 i).
+__device__ __forceinline__ void lds_load16(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
+}
+
+// 8 numbers as operands: rounded to binary16, and with Low what that leaves of them.
+template <bool Low>
+__device__ __forceinline__ void split8(const float (&v)[8], h16x8& hi, h16x8& lo) {
+    u32x4 uh, ul;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x2 two{v[2 * i], v[2 * i + 1]};
+        const h16x2 h = __builtin_convertvector(two, h16x2);
+        uh[i] = __builtin_bit_cast(uint32_t, h);
+        if constexpr (Low) {
+            const f32x2 rest{two.x - (float)h.x, two.y - (float)h.y};
+            ul[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, h16x2));
+        }
+    }
+    hi = __builtin_bit_cast(h16x8, uh);
+    if constexpr (Low)
+        lo = __builtin_bit_cast(h16x8, ul);
 }
 
 // N words of a lane, 4 N bytes that follow each other.
@@ -162,7 +209,7 @@ __device__ __forceinline__ float lse_of(float ref, float sum) {
                        : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
 }
 
-// What is kept for 16 * NC rows of q while the tokens pass, and a step.
+// What is kept for 16 * NC rows of q while the tokens pass, and their scores.
 template <int D, int G, bool F16, int NC>
 struct State {
     static constexpr int W = D / 32;      // products over the head's width; words of k to a lane
@@ -178,8 +225,7 @@ struct State {
     int seen_lo[NC], seen_hi[NC];
     int full_lo, full_hi;     // tokens that every row sees
     f32x4 acc[NC][NJ];
-    float R[NC], l[NC], mb[NC][NG];
-    float k2, s_lim;          // the power of two of p, largest scale that it is meant for
+    float R[NC], l[NC];
 
     __device__ explicit State(const Args& args)
         : p(args), lane(threadIdx.x & 63), r(lane & 15), g(lane >> 4) {}
@@ -188,13 +234,12 @@ struct State {
     __device__ __forceinline__ void range(const Seq& sq, int first, int n, int rows, int& from,
                                           int& to) const {
         const int last = (first + n < rows ? first + n : rows) - 1, at0 = sq.len - sq.n;
-        to = first >= rows ? 0 : p.a.causal ? clampi(at0 + last / p.share + 1, 0, sq.len) : sq.len;
-        from = p.a.window > 0 ? clampi(at0 + first / p.share + 1 - p.a.window, 0, to) : 0;
+        to = first >= rows ? 0 : p.a.causal ? clampi(at0 + p.share.div(last) + 1, 0, sq.len) : sq.len;
+        from = p.a.window > 0 ? clampi(at0 + p.share.div(first) + 1 - p.a.window, 0, to) : 0;
     }
 
     // Rows of q of this wave: `first` is the first of them among the sequence's rows.
     __device__ __forceinline__ void load_q(const Seq& sq, int first, int rows) {
-        range(sq, first, 16 * NC, rows, lo, hi);
         full_lo = 0;
         full_hi = 1 << 30;
         // a negative scale is that of -q
@@ -203,12 +248,11 @@ struct State {
         for (int c = 0; c < NC; ++c) {
             const int row = first + 16 * c + r;
             const bool in = row < rows;
-            const int qi = in ? row / p.share : 0, hd = in ? row % p.share : 0;
+            const int qi = in ? p.share.div(row) : 0, hd = in ? p.share.mod(row) : 0;
             const uint16_t* x = p.a.q + (int64_t)(sq.row0 + qi) * p.a.ldq +
-                                (int64_t)(head * p.share + hd) * p.a.hsq + 8 * g;
+                                (int64_t)(head * (int)p.share.d + hd) * p.a.hsq + 8 * g;
             float f[8 * W];
             float top = 0.0f;
-            bool fine = true;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 const u32x4 w = in ? ld16(x + 32 * k) : u32x4{};
@@ -217,35 +261,40 @@ struct State {
                 else
                     unpack_bf16x8(w, f + 8 * k);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float m = __builtin_fabsf(f[8 * k + i]);
-                    fine = fine && m < __builtin_inff();
-                    top = __builtin_fmaxf(top, m);
-                    f[8 * k + i] *= sign;
-                }
+                for (int i = 0; i < 8; ++i)
+                    top = __builtin_fmaxf(top, __builtin_fabsf(f[8 * k + i]));
             }
             top = quarter_max(top);
-            const bool all_fine = quarter_sum(fine ? 0.0f : 1.0f) == 0.0f;
-            const int e = all_fine ? __builtin_amdgcn_frexp_expf(top) : 0;
+            // rows below 2^-100 go without the bits that this leaves them
+            const int e = clampi(__builtin_amdgcn_frexp_expf(top), -100, 128);
+            const float by = sign * __builtin_ldexpf(1.0f, 14 - e);
             fac[c] = sign == 0.0f ? 1.0f : __builtin_ldexpf(__builtin_fabsf(p.scale2), 10 + e);
+            float bad = 0.0f;
 #pragma unroll
             for (int k = 0; k < NG; ++k) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8 * W / NG; ++i)
-                    sum += __builtin_ldexpf(f[k * (8 * W / NG) + i], -10 - e);
-                qs[c][k] = all_fine ? quarter_sum(sum) : __builtin_nanf("");
+                for (int i = k * (8 * W / NG); i < (k + 1) * (8 * W / NG); ++i) {
+                    f[i] *= by;
+                    sum += f[i];
+                }
+                sum = quarter_sum(sum);
+                bad += sum * 0.0f;      // a NaN or an infinity in any of the row's groups
+                qs[c][k] = sum * 0x1p-24f;
             }
 #pragma unroll
+            for (int k = 0; k < NG; ++k)
+                qs[c][k] += bad;
+#pragma unroll
             for (int k = 0; k < W; ++k) {
-                h16x8 o;
+                u32x4 o;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int sh = (i & 1 ? 10 : 14) - e;
-                    o[2 * i] = (_Float16)__builtin_ldexpf(f[8 * k + i], sh);
-                    o[2 * i + 1] = (_Float16)__builtin_ldexpf(f[8 * k + i + 4], sh);
+                    const float z = i & 1 ? 0x1p-4f : 1.0f;
+                    const f32x2 two{f[8 * k + i] * z, f[8 * k + i + 4] * z};
+                    o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, h16x2));
                 }
-                q[c][k] = o;
+                q[c][k] = __builtin_bit_cast(h16x8, o);
             }
             const int at = sq.len - sq.n + qi;      // the row's place
             seen_hi[c] = p.a.causal && in ? (at + 1 < sq.len ? at + 1 : sq.len) : sq.len;
@@ -271,22 +320,15 @@ struct State {
             R[c] = -__builtin_inff();
             l[c] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < NG; ++k)
-                mb[c][k] = 0.0f;
-#pragma unroll
             for (int j = 0; j < NJ; ++j)
                 acc[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        k2 = 0.0f;
-        s_lim = 0.0f;
     }
 
-    // 32 tokens from `tok` on.  What the source gives: k(h, w) and v(j), operands; k_scales<group>
-    // and v_scales<group>, scale and least value of the 8 tokens of this quarter wave (of values
-    // m + 8 s); s_max, the largest scale of values among this lane's.  ok: the 8 tokens' page is there.
-    template <bool MASK, typename Src>
-    __device__ __forceinline__ void step(const Src& src, int tok, bool ok) {
-        float x[NC][8];
+    // Scores, over fac, of 32 tokens: those of this quarter wave's 8 tokens.  What the source gives:
+    // k(h, w), operands, and k_scales<group>, scale and least value of the 8 tokens.
+    template <typename Src>
+    __device__ __forceinline__ void scores(const Src& src, float (&x)[NC][8]) const {
         unroll<NG>([&](auto gi) {
             constexpr int k = decltype(gi)::value;
             f32x4 a[NC][2];
@@ -315,18 +357,16 @@ struct State {
                                              k == 0 ? s[i] * b : __builtin_fmaf(s[i], b, x[c][i]));
                 }
         });
-        float top[NC];
-        bool raise = src.s_max > s_lim;
+    }
+    // Whether row c sees token t of a page that is there.
+    __device__ __forceinline__ bool sees(int c, int t) const {
+        return t >= seen_lo[c] && t < seen_hi[c] && t < hi;
+    }
+    // The largest scores, and whether one passes its reference by more than kRaise.
+    __device__ __forceinline__ bool tops(const float (&x)[NC][8], float (&top)[NC]) const {
+        bool raise = false;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            if constexpr (MASK) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int t = tok + 8 * g + i;
-                    const bool in = ok && t >= seen_lo[c] && t < seen_hi[c] && t < hi;
-                    x[c][i] = in ? x[c][i] : -__builtin_inff();
-                }
-            }
             top[c] = x[c][0];
 #pragma unroll
             for (int i = 1; i < 8; ++i)
@@ -334,95 +374,14 @@ struct State {
             top[c] *= fac[c];
             raise = raise || top[c] > R[c] + kRaise;
         }
-        if (__any(raise))
-            new_reference(top, src.s_max);
-        float pr[NC][8];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float ref = R[c] == -__builtin_inff() ? 0.0f : R[c] - k2;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                pr[c][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[c][i], fac[c], -ref));
-                sum += pr[c][i];
-            }
-            l[c] += sum;
-        }
-        unroll<NG>([&](auto gi) {
-            constexpr int k = decltype(gi)::value;
-            h16x8 ph[NC], pl[NC];
-            float s[8], m[8];
-            src.template v_scales<k>(s, m);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                float ps[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ps[i] = pr[c][i] * s[i];
-                    if constexpr (MASK) {
-                        // what a row does not see has no effect on it, a scale of NaN neither
-                        const bool in = !(x[c][i] == -__builtin_inff());
-                        ps[i] = in ? ps[i] : 0.0f;
-                        mb[c][k] += in ? pr[c][i] * m[i] : 0.0f;
-                    } else {
-                        mb[c][k] = __builtin_fmaf(pr[c][i], m[i], mb[c][k]);
-                    }
-                }
-                u32x4 uh, ul;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x2 two{ps[2 * i], ps[2 * i + 1]};
-                    const h16x2 h = __builtin_convertvector(two, h16x2);
-                    uh[i] = __builtin_bit_cast(uint32_t, h);
-                    if constexpr (F16) {
-                        const f32x2 rest{two.x - (float)h.x, two.y - (float)h.y};
-                        ul[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, h16x2));
-                    }
-                }
-                ph[c] = __builtin_bit_cast(h16x8, uh);
-                if constexpr (F16)
-                    pl[c] = __builtin_bit_cast(h16x8, ul);
-            }
-#pragma unroll
-            for (int j = k * (NJ / NG); j < (k + 1) * (NJ / NG); ++j) {
-                const h16x8 o = src.v(j);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if constexpr (F16)
-                        acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, pl[c], acc[c][j], 0, 0, 0);
-                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
-                }
-            }
-        });
+        return raise;
     }
-
-    // Raises the rows' references to their largest scores, and fits 2^k to the largest scale.
-    __device__ __forceinline__ void new_reference(const float (&top)[NC], float s_max) {
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            s_max = __builtin_fmaxf(s_max, __shfl_xor(s_max, d));
-        float up = 0.0f;
-        if (s_max > s_lim) {
-            const int e = clampi(__builtin_amdgcn_frexp_expf(s_max), -93, 107);
-            up = (float)(7 - e) - k2;
-            k2 = (float)(7 - e);
-            s_lim = __builtin_ldexpf(1.0f, e);
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float m = __builtin_fmaxf(R[c], quarter_max(top[c]));
-            const float by = R[c] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(R[c] - m + up);
-            R[c] = m;
-            l[c] *= by;
-#pragma unroll
-            for (int k = 0; k < NG; ++k)
-                mb[c][k] *= by;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[c][j][i] *= by;
-        }
+    // Raises row c's reference; what its sums are to be multiplied with.
+    __device__ __forceinline__ float raised(int c, float top) {
+        const float m = __builtin_fmaxf(R[c], quarter_max(top));
+        const float by = R[c] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(R[c] - m);
+        R[c] = m;
+        return by;
     }
 
     template <int N, typename F>
@@ -434,23 +393,12 @@ struct State {
         (f(std::integral_constant<int, I>{}), ...);
     }
 
-    // The row's result before the division, numbers 16j + 4g .. +3.
-    __device__ __forceinline__ f32x4 result(int c, int j, const float (&least)[NG]) const {
-        f32x4 o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(acc[c][j][i], j & 1 ? 0x1p-4f : 1.0f, least[j / (NJ / NG)]);
-        return o;
-    }
-    // The reference that the sums are relative to.
-    __device__ __forceinline__ float reference(int c) const { return R[c] - k2; }
-
     __device__ __forceinline__ int64_t cell(const Seq& sq, int row) const {
-        return (int64_t)(sq.row0 + row / p.share) * p.a.heads + head * p.share + row % p.share;
+        return (int64_t)(sq.row0 + p.share.div(row)) * p.a.heads + head * (int)p.share.d + p.share.mod(row);
     }
     __device__ __forceinline__ uint16_t* out_of(const Seq& sq, int row) const {
-        return p.a.out + (int64_t)(sq.row0 + row / p.share) * p.a.ldo +
-               (int64_t)(head * p.share + row % p.share) * p.a.hso;
+        return p.a.out + (int64_t)(sq.row0 + p.share.div(row)) * p.a.ldo +
+               (int64_t)(head * (int)p.share.d + p.share.mod(row)) * p.a.hso;
     }
     __device__ __forceinline__ void put_lse(const Seq& sq, int row, float ref, float sum) const {
         if (p.a.lse)
@@ -462,8 +410,8 @@ struct State {
 struct Walk {
     int idx, off, dq, dr;
     Walk() = default;
-    __device__ __forceinline__ Walk(int block, int stride, int bpp)
-        : idx(block / bpp), off(block % bpp), dq(stride / bpp), dr(stride % bpp) {}
+    __device__ __forceinline__ Walk(int block, int stride, const Div& bpp)
+        : idx(bpp.div(block)), off(bpp.mod(block)), dq(bpp.div(stride)), dr(bpp.mod(stride)) {}
     __device__ __forceinline__ void step(int bpp) {
         idx += dq;
         off += dr;
@@ -479,53 +427,74 @@ struct Walk {
 struct Place {
     int tile, head, split, seq;
     __device__ __forceinline__ explicit Place(const Args& p) {
-        tile = p.tiles - 1 - (int)(blockIdx.x / (uint32_t)p.units);
-        int unit = (int)(blockIdx.x % (uint32_t)p.units);
-        head = unit % p.a.c.heads;
-        unit /= p.a.c.heads;
-        split = unit % p.splits;
-        seq = unit / p.splits;
+        tile = p.tiles - 1 - p.units.div(blockIdx.x);
+        const int unit = p.units.mod(blockIdx.x), rest = p.heads.div(unit);
+        head = p.heads.mod(unit);
+        split = p.by_splits.mod(rest);
+        seq = p.by_splits.div(rest);
     }
 };
 
-// Blocks [b0, b1) of 8 tokens of a split of tokens [lo, hi), in whole steps of `unit` blocks.
-__device__ __forceinline__ void split_blocks(int lo, int hi, int split, int splits, int unit, int& b0,
+// Blocks [b0, b1) of 8 tokens of a split of tokens [lo, hi), in whole turns of `unit` blocks; b0
+// is a multiple of 4.
+__device__ __forceinline__ void split_blocks(int lo, int hi, int split, const Div& splits, int unit, int& b0,
                                              int& b1) {
-    const int first = lo / 8, n = (hi + 7) / 8 - first;
-    const int per = ((n + splits - 1) / splits + unit - 1) / unit * unit;
+    const int first = lo / 32 * 4, n = (hi + 7) / 8 - first;
+    const int per = (splits.div(n + (int)splits.d - 1) + unit - 1) / unit * unit;
     b0 = first + split * per;
     b1 = b0 + per < first + n ? b0 + per : first + n;
 }
 
 // ---- few rows: the waves of a workgroup share its tokens --------------------------------------
 //
-// Each wave takes every fourth step of the workgroup's tokens, straight from memory to
-// operands, one step loaded ahead; the waves' results join through LDS.  Scales are loaded
-// once a quarter wave, one word or a few to a lane, and broadcast as DPP operands.
+// Each wave takes every fourth step of the workgroup's tokens and keeps to itself: a ring of
+// `Depth` steps in LDS, filled by global-to-LDS loads (16 bytes a lane, in the cache's own order),
+// so that the next steps are on their way without a register; no barriers until the waves'
+// results meet.
+// Chunks of 16 bytes are permuted within a block so that neither operand's reads meet a
+// bank conflict.  Scales: one word or a few to a lane of a quarter wave, broadcast as DPP operands.
 template <int D, int G, bool F16, int NC>
 struct Tokens : State<D, G, F16, NC> {
     using S = State<D, G, F16, NC>;
-    using S::W, S::NJ, S::NG, S::p, S::r, S::g, S::head, S::lo, S::hi;
+    using S::W, S::NJ, S::NG, S::p, S::lane, S::r, S::g, S::head, S::lo, S::hi;
+    using S::acc, S::R, S::l, S::fac;
 
-    const int32_t* table;
+    static constexpr int kChunks = D / 4;               // of 16 bytes, in a block of 8 tokens
+    static constexpr int kJ = D / 64;                   // loads of k, and of v, in a step
+    static constexpr int kLoads = 2 * kJ + NG;
+    static constexpr int kV = 16 * D, kS = 32 * D, kSlot = 32 * D + 256 * NG;
+    // workgroups that a compute unit holds, and the steps that leave room for them
+    static constexpr int kGroups = NC == 1 && D <= 128 ? 3 : 2;
+    static constexpr int kMost = 160 * 1024 / (kGroups * kWaves * kSlot);
+    static constexpr int Depth = kMost > 4 ? 4 : kMost;
+    static_assert(Depth >= 2, "a step is used while the next is loaded");
+    static constexpr int kJoin = (kWaves * 16 * (D + 4) + kWaves * 16 * 2) * 4;
+    static constexpr int kLds = kWaves * Depth * kSlot > kJoin ? kWaves * Depth * kSlot : kJoin;
 
-    struct Tile {
-        uint32_t k[2][W], v[NJ], s[NG];
-        int tok;
-        bool ok;
-    };
+    // Where chunk q of a block of k (the b-th of its step) and of v lies; each its own inverse.
+    static __device__ __forceinline__ uint32_t k_slot(uint32_t q, uint32_t b) {
+        if constexpr (D == 64)
+            return q ^ ((b & 1) * 8 + (b >> 1 & 1));
+        else if constexpr (D == 128)
+            return q ^ b;
+        else
+            return q ^ ((q >> 4 & 1) * 4 + b);
+    }
+    static __device__ __forceinline__ uint32_t v_slot(uint32_t q) {
+        return D == 64 ? q : D == 128 ? q ^ (q >> 4 & 1) : q ^ (q >> 4 & 3);
+    }
 
     struct Src {
-        const Tile& t;
+        uint32_t kw[2][W], vw[NJ];
         float ss[NG], sm[NG], s_max;
 
-        __device__ __forceinline__ h16x8 k(int h, int w) const { return codes8(t.k[h][w]); }
+        __device__ __forceinline__ h16x8 k(int h, int w) const { return codes8(kw[h][w]); }
         __device__ __forceinline__ h16x8 v(int j) const {
             u32x4 op;
 #pragma unroll
             for (int tp = 0; tp < 4; ++tp) {
-                const uint32_t w = t.v[tp * (D / 64) + j / 4];
-                op[tp] = centred(j % 4 >= 2 ? w >> 8 : w, j & 1);
+                const uint32_t w = vw[tp * (D / 64) + j / 4];
+                op[tp] = (j % 4 >= 2 ? w >> 8 : w) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
             }
             return __builtin_bit_cast(h16x8, op);
         }
@@ -544,15 +513,35 @@ struct Tokens : State<D, G, F16, NC> {
         __device__ __forceinline__ void v_scales(float (&s)[8], float (&m)[8]) const {
             eight<8 * NG + 8 * K>(s, m, std::make_integer_sequence<int, 8>{});
         }
-        __device__ __forceinline__ Src(const Tile& tile, bool mask, int lo, int hi, int r, int g)
-            : t(tile), s_max(0.0f) {
-            const int tok = t.tok + 8 * g + (r & 7);
-            const bool in = !mask || (t.ok && tok >= lo && tok < hi);
+        // `in`: some row sees the token whose words this lane has.
+        __device__ __forceinline__ Src(const char* slot, bool in, int r, int g) : s_max(0.0f) {
+            const uint32_t b = (uint32_t)r >> 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t row = (r & 3) + 4 * h;
+                if constexpr (W == 2) {
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(
+                        slot + b * 4 * D + 16 * k_slot(row * 2 + (g >> 1), b) + 8 * (g & 1));
+                    kw[h][0] = x.x;
+                    kw[h][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i)
+                        put(kw[h] + 4 * i, slot + b * 4 * D +
+                                               16 * k_slot(row * (D / 32) + g * (W / 4) + i, b));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NJ / 4; ++i)
+                put(vw + 4 * i, slot + kV + g * 4 * D + 16 * v_slot(r * (NJ / 4) + i));
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
+                const int e = 16 * i + r, which = e >> 3;       // groups of keys, then of values
+                const uint32_t w =
+                    *reinterpret_cast<const uint32_t*>(slot + kS + (which * 32 + 8 * g + (e & 7)) * 4);
                 // 0 for tokens that no row sees
-                ss[i] = in ? lo16<F16>(t.s[i]) : 0.0f;
-                sm[i] = in ? hi16<F16>(t.s[i]) : 0.0f;
+                ss[i] = in ? lo16<F16>(w) : 0.0f;
+                sm[i] = in ? hi16<F16>(w) : 0.0f;
                 // registers of values: the upper half, or the upper lanes of the only one
                 if (NG == 1 ? r >= 8 : 2 * i >= NG) {
                     const float m = __builtin_fabsf(ss[i]);
@@ -561,101 +550,266 @@ struct Tokens : State<D, G, F16, NC> {
                 }
             }
         }
+        static __device__ __forceinline__ void put(uint32_t* w, const char* at) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = x[i];
+        }
     };
+
+    float mb[NC][NG];
+    float k2, s_lim;          // the power of two of p, largest scale that it is meant for
+
+    // 32 tokens from `tok` on.  ok: the 8 tokens' page is there.  mask (uniform): not every row sees
+    // every token.  Scales of values that are not finite then go into the score of the rows that
+    // see them, as a NaN, and out of the others' way.
+    __device__ __forceinline__ void step(const Src& src, int tok, bool ok, bool mask) {
+        float x[NC][8];
+        this->scores(src, x);
+        if (mask) {
+            float bad[8];
+            S::template unroll<NG>([&](auto gi) {
+                constexpr int k = decltype(gi)::value;
+                float s[8], m[8];
+                src.template v_scales<k>(s, m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float z = s[i] * 0.0f + m[i] * 0.0f;      // 0, or NaN
+                    bad[i] = k == 0 ? z : bad[i] + z;
+                }
+            });
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[c][i] = ok && this->sees(c, tok + 8 * g + i) ? x[c][i] + bad[i] : -__builtin_inff();
+        }
+        float top[NC];
+        const bool raise = this->tops(x, top);
+        if (__any(raise || src.s_max > s_lim))
+            new_reference(top, src.s_max);
+        float pr[NC][8];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float ref = R[c] == -__builtin_inff() ? 0.0f : R[c] - k2;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                pr[c][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[c][i], fac[c], -ref));
+                sum += pr[c][i];
+            }
+            l[c] += sum;
+        }
+        S::template unroll<NG>([&](auto gi) {
+            constexpr int k = decltype(gi)::value;
+            h16x8 ph[NC], pl[NC];
+            float s[8], m[8];
+            src.template v_scales<k>(s, m);
+            if (mask) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool fine = s[i] * 0.0f + m[i] * 0.0f == 0.0f;
+                    s[i] = fine ? s[i] : 0.0f;
+                    m[i] = fine ? m[i] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float ps[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ps[i] = pr[c][i] * s[i];
+                    mb[c][k] = __builtin_fmaf(pr[c][i], m[i], mb[c][k]);
+                }
+                split8<F16>(ps, ph[c], pl[c]);
+            }
+#pragma unroll
+            for (int j = k * (NJ / NG); j < (k + 1) * (NJ / NG); ++j) {
+                const h16x8 o = src.v(j);
+                // -8 times the power of two of an even, of an odd block's codes
+                const uint32_t e = j & 1 ? 0x80808080u : 0x80088008u;
+                const h16x8 eight = __builtin_bit_cast(h16x8, u32x4{e, e, e, e});
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    if constexpr (F16) {
+                        acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(eight, pl[c], acc[c][j], 0, 0, 0);
+                        acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, pl[c], acc[c][j], 0, 0, 0);
+                    }
+                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(eight, ph[c], acc[c][j], 0, 0, 0);
+                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
+                }
+            }
+        });
+    }
+
+    // Raises the rows' references to their largest scores, and fits 2^k to the largest scale.
+    __device__ __forceinline__ void new_reference(const float (&top)[NC], float s_max) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            s_max = __builtin_fmaxf(s_max, __shfl_xor(s_max, d));
+        float up = 1.0f;
+        if (s_max > s_lim) {
+            const int e = clampi(__builtin_amdgcn_frexp_expf(s_max), -93, 107);
+            up = __builtin_amdgcn_exp2f((float)(7 - e) - k2);
+            k2 = (float)(7 - e);
+            s_lim = __builtin_ldexpf(1.0f, e);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float by = this->raised(c, top[c]), both = by == 0.0f ? 0.0f : by * up;
+            l[c] *= both;
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+                mb[c][k] *= both;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[c][j][i] *= both;
+        }
+    }
+
+    // The row's result before the division, numbers 16j + 4g .. +3.
+    __device__ __forceinline__ f32x4 result(int c, int j, const float (&least)[NG]) const {
+        f32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = __builtin_fmaf(acc[c][j][i], j & 1 ? 0x1p20f : 0x1p24f, least[j / (NJ / NG)]);
+        return o;
+    }
+
+    // Where the blocks of this wave's next 16 steps lie, one block to a lane (four to a step): found
+    // once for all of them, and handed to the loading lanes by permutes.
+    const int32_t* table;
+    int b0, stride, steps;
+    int64_t code, scale;        // bytes from the arrays' starts
+    uint64_t there;             // whether the blocks' pages are
+    uint32_t oks;               // the same for the steps in the ring, 4 bits to a slot
 
     __device__ explicit Tokens(const Args& args) : S(args) {}
 
-    __device__ __forceinline__ int page_at(int idx) const {
-        return idx < p.a.table_cols ? table[idx] : -1;
+    __device__ __forceinline__ void find_pages(int n) {
+        const bq_kv_i4& c = p.a.c;
+        // behind the last step: that one again
+        const int s = n + (lane >> 2), b = b0 + (s < steps ? s : steps - 1) * stride + (lane & 3);
+        const int idx = p.bpp.div(b), o = b - idx * (int)p.bpp.d;
+        const int page = idx < p.a.table_cols ? table[idx] : -1;
+        const bool in = (uint32_t)page < (uint32_t)c.pages;
+        // a page outside the pool: page 0 is read, and no row sees it
+        const int64_t at = in ? page : 0;
+        code = at * c.page_stride + (int64_t)head * c.head_stride + (int64_t)o * (4 * D);
+        scale = 2 * (at * c.spage_stride + (int64_t)head * c.shead_stride) + o * 32;
+        there = __ballot(in);
+    }
+    // The value of block `b` of the `rel`-th step found.
+    static __device__ __forceinline__ int64_t from(int64_t v, int rel, uint32_t b) {
+        const int at = 16 * rel + 4 * b;
+        const uint32_t lo = __builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)v);
+        const uint32_t hi = __builtin_amdgcn_ds_bpermute(at, (int)(v >> 32));
+        return (int64_t)((uint64_t)hi << 32 | lo);
     }
 
-    __device__ __forceinline__ Tile load(const Walk& wk, const Walk& wv, int pk, int pv, int tok) const {
-        Tile t;
+    // Loads step n into slot s.  The count of loads is always the same.
+    __device__ __forceinline__ void issue(char* ring, int s, int n) {
+        const int rel = n & 15;
+        if (rel == 0)
+            find_pages(n);
         const bq_kv_i4& c = p.a.c;
-        t.tok = tok;
-        t.ok = (uint32_t)pv < (uint32_t)c.pages;
-        // a page outside the pool: page 0 is read, and no row sees it
-        const int64_t ik = (uint32_t)pk < (uint32_t)c.pages ? pk : 0, iv = t.ok ? pv : 0;
-        const uint8_t* k = c.k + ik * c.page_stride + (int64_t)head * c.head_stride +
-                           (int64_t)wk.off * (8 * D / 2) + (r & 3) * (D / 2) + g * (D / 8);
+        char* slot = ring + s * kSlot;
+        oks = (oks & ~(15u << (4 * s))) | (uint32_t)(there >> (4 * rel) & 15u) << (4 * s);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            ld_words<W>(k + h * 4 * (D / 2), t.k[h]);
-        ld_words<NJ>(c.v + iv * c.page_stride + (int64_t)head * c.head_stride +
-                         (int64_t)wv.off * (8 * D / 2) + r * (D / 4), t.v);
-        const int64_t so = iv * c.spage_stride + (int64_t)head * c.shead_stride;
+        for (int j = 0; j < kJ; ++j) {
+            const uint32_t q = j * 64 + lane, b = q / kChunks;
+            const int64_t at = from(code, rel, b);
+            lds_load16(c.k + at + 16 * k_slot(q % kChunks, b), slot + 1024 * j);
+            lds_load16(c.v + at + 16 * v_slot(q % kChunks), slot + kV + 1024 * j);
+        }
+        const int64_t at = from(scale, rel, (lane & 31) >> 3) + 4 * (lane & 7);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            const int e = 16 * i + r;
-            const bool of_v = e >= 8 * NG;
-            const int at = of_v ? e - 8 * NG : e;
-            const uint16_t* s = (of_v ? c.vs : c.ks) + so +
-                                2 * ((int64_t)(at >> 3) * c.page_size + wv.off * 8 + (at & 7));
-            t.s[i] = *reinterpret_cast<const uint32_t*>(s);
-        }
-        return t;
-    }
-
-    // All steps over blocks of 8 tokens [b0, b1), `stride` blocks apart.
-    __device__ __forceinline__ void walk(int b0, int b1, int stride) {
-        if (b0 >= b1)
-            return;
-        const int bpp = p.bpp;
-        Walk wk(b0 + (r >> 2), stride, bpp), wv(b0 + g, stride, bpp);
-        Tile t = load(wk, wv, page_at(wk.idx), page_at(wv.idx), b0 * 8);
-        wk.step(bpp);
-        wv.step(bpp);
-        int pk = page_at(wk.idx), pv = page_at(wv.idx);
-        for (int b = b0; b < b1; b += stride) {
-            Tile next = t;
-            if (b + stride < b1) {
-                next = load(wk, wv, pk, pv, (b + stride) * 8);
-                wk.step(bpp);
-                wv.step(bpp);
-                pk = page_at(wk.idx);
-                pv = page_at(wv.idx);
-            }
-            if (t.tok >= this->full_lo && t.tok + kStep <= this->full_hi && __all(t.ok))
-                this->template step<false>(Src(t, false, lo, hi, r, g), t.tok, true);
-            else
-                this->template step<true>(Src(t, true, lo, hi, r, g), t.tok, t.ok);
-            t = next;
+            const int which = 2 * i + (lane >> 5);
+            const uint8_t* s0 = reinterpret_cast<const uint8_t*>(which < NG ? c.ks : c.vs);
+            lds_load4(s0 + at + 4 * (int64_t)c.page_size * (which < NG ? which : which - NG),
+                      slot + kS + 256 * i);
         }
     }
 
-    __device__ __forceinline__ void run(float* lds) {
+    // Steps over blocks of 8 tokens [first, end), every fourth: the first ones are sent for.
+    __device__ __forceinline__ void begin(char* ring, int first, int end) {
+        b0 = first;
+        stride = 4 * kWaves;
+        steps = first < end ? (end - first + stride - 1) / stride : 0;
+        oks = 0;
+        if (steps > 0) {
+#pragma unroll
+            for (int d = 0; d < Depth - 1; ++d)
+                issue(ring, d, d);
+        }
+    }
+    __device__ __forceinline__ void walk(char* ring) {
+        int s = 0;
+        for (int n = 0; n < steps; ++n) {
+            // what was read of the slot that is loaded now has arrived
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue(ring, s == 0 ? Depth - 1 : s - 1, n + Depth - 1);
+            // this step has landed when only those after it are outstanding
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((Depth - 1) * kLoads) : "memory");
+            const uint32_t ok = oks >> (4 * s) & 15u;
+            const int tok = 8 * (b0 + n * stride);
+            const bool mask = !(ok == 15u && tok >= this->full_lo && tok + kStep <= this->full_hi);
+            const bool mine = ok >> g & 1u;
+            const int t = tok + 8 * g + (r & 7);
+            this->step(Src(ring + s * kSlot, !mask || (mine && t >= lo && t < hi), r, g), tok, mine, mask);
+            s = s == Depth - 1 ? 0 : s + 1;
+        }
+        // nothing lands in LDS after the end
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    __device__ __forceinline__ void run(char* lds) {
         const AttnI4& a = p.a;
         const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
         const Place at(p);
         head = at.head;
         const Seq sq = seq_of(a, at.seq);
-        const int rows = sq.n * p.share, first = at.tile * 16 * NC;
+        const int rows = sq.n * (int)p.share.d, first = at.tile * 16 * NC;
         if (first >= rows)
             return;
         table = a.table + (int64_t)at.seq * a.ldt;
+        char* ring = lds + wave * Depth * kSlot;
+        int from, to;
+        this->range(sq, first, 16 * NC, rows, lo, hi);
+        split_blocks(lo, hi, at.split, p.by_splits, 4 * kWaves, from, to);
+        begin(ring, from + 4 * wave, to);
         this->load_q(sq, first, rows);
-        int b0, b1;
-        split_blocks(lo, hi, at.split, p.splits, 4 * kWaves, b0, b1);
-        walk(b0 + 4 * wave, b1, 4 * kWaves);
+        k2 = 0.0f;
+        s_lim = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+                mb[c][k] = 0.0f;
+        walk(ring);
         const bool whole = p.splits == 1;
-        // the waves' parts: [wave][row][D + 4], then (R, sum)
+        // the waves' parts, where the rings were: [wave][row][D + 4], then (R, sum)
         constexpr int LD = D + 4;
-        float* part = lds + (wave * 16 + r) * LD;
-        float* ml = lds + kWaves * 16 * LD;
+        float* all = reinterpret_cast<float*>(lds);
+        float* part = all + (wave * 16 + r) * LD;
+        float* ml = all + kWaves * 16 * LD;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float least[NG];
             const float sum = quarter_sum(this->l[c]);
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                least[k] = quarter_sum(this->mb[c][k]);
-            if (c > 0)
-                __syncthreads();
+                least[k] = quarter_sum(mb[c][k]);
+            __syncthreads();
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                *reinterpret_cast<f32x4*>(part + 16 * j + 4 * g) = this->result(c, j, least);
+                *reinterpret_cast<f32x4*>(part + 16 * j + 4 * g) = result(c, j, least);
             if (g == 0)
-                *reinterpret_cast<f32x2*>(ml + 2 * (wave * 16 + r)) = f32x2{this->reference(c), sum};
+                *reinterpret_cast<f32x2*>(ml + 2 * (wave * 16 + r)) = f32x2{R[c] - k2, sum};
             __syncthreads();
             const int mine = threadIdx.x >> 4, seg = threadIdx.x & 15;
             const int row = first + 16 * c + mine;
@@ -680,7 +834,7 @@ struct Tokens : State<D, G, F16, NC> {
 #pragma unroll
                 for (int v = 0; v < kWaves; ++v) {
                     const f32x4 z =
-                        *reinterpret_cast<const f32x4*>(lds + (v * 16 + mine) * LD + 64 * j + 4 * seg);
+                        *reinterpret_cast<const f32x4*>(all + (v * 16 + mine) * LD + 64 * j + 4 * seg);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         y[i] = __builtin_fmaf(w[v], z[i], y[i]);
@@ -701,51 +855,63 @@ struct Tokens : State<D, G, F16, NC> {
 };
 
 template <int D, int G, bool F16, int NC>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_tokens(Args p) {
-    __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * 16 * 2];
+__global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, NC>::kGroups)) void k_attn_tokens(Args p) {
+    __shared__ __align__(16) char lds[Tokens<D, G, F16, NC>::kLds];
     Tokens<D, G, F16, NC> k(p);
     k.run(lds);
 }
 
 // ---- many rows: the waves share the tokens' operands ------------------------------------------
 //
-// Each wave has 16 * NC rows of its own, and all of them see the same tokens: T a turn, which the
-// workgroup makes into operands once, in LDS (two buffers, one barrier a turn: while a turn's
+// Each of 8 waves has 16 * NC rows of its own, and all of them see the same tokens: T a turn, which
+// the workgroup makes into operands once, in LDS (two buffers, one barrier a turn: while a turn's
 // operands are used, the codes of the next one are unpacked and those after it loaded).  An
-// operand is 64 lanes * 16 bytes in the lanes' order, so neither side meets a bank conflict; scales
-// lie there in binary32.
+// operand is 64 lanes * 16 bytes in the lanes' order, so neither side meets a bank conflict.  Four
+// waves unpack values, the other four keys and their scales.
+//
+// Values become binary16 numbers here, (c - 8) s + (m + 8 s) in one rounding, so that p needs no
+// scale of each group.  For that the 8 tokens of a block take a power of two 2^b that brings their
+// largest to just below 2^15 (1 in the _f16 kernels, whose values fit); a quarter wave's 8 tokens of
+// p are one block, so p takes 2^(k - b) there, k the least b so far.
 template <int D, int G, bool F16, int NC>
 struct Rows : State<D, G, F16, NC> {
     using S = State<D, G, F16, NC>;
     using S::W, S::NJ, S::NG, S::p, S::lane, S::r, S::g, S::head, S::lo, S::hi;
+    using S::acc, S::R, S::l, S::fac;
 
+    static constexpr int kRowWaves = 8;
     static constexpr int T = D == 256 ? 32 : 64;        // tokens a turn
     static constexpr int NS = T / kStep;                // steps a turn
-    static constexpr int Parts = kWaves / NS;           // waves that unpack a step
+    static constexpr int Parts = 4 / NS;                // waves of a kind that unpack a step
     static constexpr int KW = 2 * W / Parts;            // words of k that a lane unpacks
     static constexpr int VB = NJ / Parts;               // blocks of v that a wave unpacks
-    static constexpr int SW = (2 * NG * T + kThreads - 1) / kThreads;   // words of scales to a thread
+    static constexpr int GV = 16 * VB > G ? 16 * VB / G : 1;    // groups that they are in
+    static constexpr int NB = NG > 1 ? NG / 2 : 1;      // words of scales to a lane, for the largest
     static constexpr int kOperand = 64 * 16;            // bytes
-    // a buffer: operands of k [step][h][w], of v [step][j], scales [ks, km, vs, vm][group][T], then
-    // whether the pages of the 8-token blocks are there
+    // a buffer: operands of k [step][h][w], of v [step][j], scale and least value of k [2][group][T],
+    // then b and whether the page is there for each block of 8 tokens
     static constexpr int kV = NS * 2 * W * kOperand;
     static constexpr int kS = kV + NS * NJ * kOperand;
-    static constexpr int kOk = kS + 4 * NG * T * 4;
-    static constexpr int kBuffer = kOk + 32;
+    static constexpr int kB = kS + 2 * NG * T * 4;
+    static constexpr int kBuffer = kB + 64;
+    static_assert(NG * T <= 256, "an entry of the keys' scales to a lane");
+    static constexpr float kUp = 6.0f;      // p is up to 2^(kRaise + kUp)
 
     const int32_t* table;
-    int wave, wg_lo, wg_hi;
+    int wave, step_of, part_of;
+    int wg_lo, wg_hi;
+    float k2;                   // the k above
 
+    // What a lane has loaded of a turn.  Of values: codes, scales of its groups' 8 tokens, scales of
+    // one or a few of all groups; of keys: codes, an entry's scales of key and value.
     struct Raw {
-        uint32_t k[KW], v[VB < 4 ? 4 : VB], s[SW];
-        bool in[SW];
+        uint32_t w[4], s[8 * GV], t[NB];
         bool ok;
     };
 
     struct Src {
         const char* buf;
         int lane, g, sub;
-        float s_max;
         __device__ __forceinline__ h16x8 k(int h, int w) const {
             return *reinterpret_cast<const h16x8*>(buf + ((sub * 2 + h) * W + w) * kOperand + lane * 16);
         }
@@ -766,21 +932,6 @@ struct Rows : State<D, G, F16, NC> {
             eight(0, K, s);
             eight(1, K, m);
         }
-        template <int K>
-        __device__ __forceinline__ void v_scales(float (&s)[8], float (&m)[8]) const {
-            eight(2, K, s);
-            eight(3, K, m);
-        }
-        __device__ __forceinline__ Src(const char* b, int lane_, int sub_)
-            : buf(b), lane(lane_), g(lane_ >> 4), sub(sub_), s_max(0.0f) {
-            // one token and group to a lane (NG <= 8: at most 4 rounds)
-            const float* at = reinterpret_cast<const float*>(buf + kS) + 2 * NG * T + sub * 32 + (lane & 31);
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-                const float m = __builtin_fabsf(at[k * T]);
-                s_max = __builtin_fmaxf(s_max, m < __builtin_inff() ? m : 0.0f);
-            }
-        }
     };
 
     __device__ explicit Rows(const Args& args) : S(args) {}
@@ -788,171 +939,272 @@ struct Rows : State<D, G, F16, NC> {
     __device__ __forceinline__ int page_at(int idx) const {
         return idx < p.a.table_cols ? table[idx] : -1;
     }
-
-    // This lane's part of a turn: step `wave / Parts`, part `wave % Parts` of its words; words of
-    // scales of the whole turn.
-    struct Walks {
-        Walk k, v, s[SW];
-    };
-
-    __device__ __forceinline__ int step_of() const { return wave / Parts; }
-    __device__ __forceinline__ int part_of() const { return wave % Parts; }
-    __device__ __forceinline__ void scale_entry(int i, int& which, int& group, int& tok) const {
-        const int e = (int)threadIdx.x + i * kThreads;
-        tok = e % T;
-        group = e / T % NG;
-        which = e / (T * NG);
+    __device__ __forceinline__ bool of_values() const { return wave < 4; }
+    // An entry of the keys' scales: token and group; -1 where there is none for this lane.
+    __device__ __forceinline__ int entry() const {
+        const int e = ((wave & 3) << 6) + lane;
+        return e < NG * T ? e : -1;
     }
 
-    __device__ __forceinline__ Raw load(const Walks& w, int tok) const {
+    // Walks: the block that this lane's codes are in, and that of its entry of scales.
+    __device__ __forceinline__ void start(int b0, Walk& wc, Walk& ws) const {
+        wc = Walk(b0 + 4 * step_of + (of_values() ? g : r >> 2), T / 8, p.bpp);
+        const int e = entry();
+        ws = Walk(b0 + (e < 0 ? 0 : e % T) / 8, T / 8, p.bpp);
+    }
+
+    __device__ __forceinline__ Raw load(const Walk& wc, const Walk& ws, int tok) const {
         Raw x;
         const bq_kv_i4& c = p.a.c;
         const uint32_t pages = (uint32_t)c.pages;
-        const int pk = page_at(w.k.idx), pv = page_at(w.v.idx);
-        const int64_t ik = (uint32_t)pk < pages ? pk : 0, iv = (uint32_t)pv < pages ? pv : 0;
-        const int64_t ho = (int64_t)head * c.head_stride;
-        // Parts == 2: the part is the half of the step's tokens (h); 4: h and half of the words
-        const int h = part_of() & 1, w0 = Parts == 4 ? (part_of() >> 1) * (W / 2) : 0;
-        ld_words<KW>(c.k + ik * c.page_stride + ho + (int64_t)w.k.off * (8 * D / 2) +
-                         ((r & 3) + 4 * h) * (D / 2) + g * (D / 8) + 4 * w0, x.k);
-        const uint8_t* v = c.v + iv * c.page_stride + ho + (int64_t)w.v.off * (8 * D / 2) + r * (D / 4);
-        if constexpr (D == 64) {
-            ld_words<4>(v, x.v);
+        const int pc = page_at(wc.idx);
+        // a page outside the pool: page 0 is read, and no row sees it
+        x.ok = (uint32_t)pc < pages;
+        const int64_t page = x.ok ? pc : 0;
+        const int64_t code = page * c.page_stride + (int64_t)head * c.head_stride + (int64_t)wc.off * (4 * D);
+        if (of_values()) {
+            const uint8_t* v = c.v + code + r * (D / 4);
+            if constexpr (D == 64) {
+                ld_words<4>(v, x.w);
+            } else {
+#pragma unroll
+                for (int tp = 0; tp < 4; ++tp)
+                    x.w[tp] = *reinterpret_cast<const uint32_t*>(v + 4 * (tp * (D / 64) + part_of));
+            }
+            const uint8_t* s = reinterpret_cast<const uint8_t*>(c.vs) +
+                               2 * (page * c.spage_stride + (int64_t)head * c.shead_stride) + 32 * wc.off;
+            const int group = part_of * VB * 16 / G;
+#pragma unroll
+            for (int k = 0; k < GV; ++k)
+                ld_words<8>(s + 4 * (int64_t)(group + k) * c.page_size, x.s + 8 * k);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int e = NG == 1 ? r & 7 : 16 * i + r;
+                x.t[i] = *reinterpret_cast<const uint32_t*>(s + 4 * ((int64_t)(e >> 3) * c.page_size + (e & 7)));
+            }
         } else {
-            // blocks [part * VB, +VB): words tp * (D / 64) + part * (VB / 4) + ..
-#pragma unroll
-            for (int tp = 0; tp < 4; ++tp)
-#pragma unroll
-                for (int i = 0; i < VB / 4; ++i)
-                    x.v[tp * (VB / 4) + i] = *reinterpret_cast<const uint32_t*>(
-                        v + 4 * (tp * (D / 64) + part_of() * (VB / 4) + i));
-        }
-        x.ok = (uint32_t)pv < pages;
-#pragma unroll
-        for (int i = 0; i < SW; ++i) {
-            int which, group, t;
-            scale_entry(i, which, group, t);
-            x.s[i] = 0;
-            x.in[i] = false;
-            if (which < 2) {
-                const int ps = page_at(w.s[i].idx);
-                x.in[i] = (uint32_t)ps < pages && tok + t >= wg_lo && tok + t < wg_hi;
-                const int64_t so = ((uint32_t)ps < pages ? (int64_t)ps : 0) * c.spage_stride +
-                                   (int64_t)head * c.shead_stride;
-                x.s[i] = *reinterpret_cast<const uint32_t*>(
-                    (which ? c.vs : c.ks) + so +
-                    2 * ((int64_t)group * c.page_size + w.s[i].off * 8 + (t & 7)));
+            const int h = part_of & 1, w0 = NS == 1 ? (part_of >> 1) * (W / 2) : 0;
+            ld_words<KW>(c.k + code + ((r & 3) + 4 * h) * (D / 2) + g * (D / 8) + 4 * w0, x.w);
+            const int e = entry();
+            x.s[0] = x.s[1] = 0;
+            if (e >= 0) {
+                const int ps = page_at(ws.idx), t = e % T;
+                if ((uint32_t)ps < pages && tok + t >= wg_lo && tok + t < wg_hi) {
+                    const int64_t at = (int64_t)ps * c.spage_stride + (int64_t)head * c.shead_stride +
+                                       2 * ((int64_t)(e / T) * c.page_size + ws.off * 8 + (t & 7));
+                    x.s[0] = *reinterpret_cast<const uint32_t*>(c.ks + at);
+                    x.s[1] = *reinterpret_cast<const uint32_t*>(c.vs + at);
+                }
             }
         }
         return x;
     }
 
-    __device__ __forceinline__ void unpack(const Raw& x, char* buf) const {
-        const int sub = step_of(), part = part_of();
-        const int h = part & 1, w0 = Parts == 4 ? (part >> 1) * (W / 2) : 0;
+    // A pair of 16-bit numbers one of which is not finite.
+    static __device__ __forceinline__ bool wild(uint32_t w) {
+        const uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u, x = w & e;
+        return (x & 0xFFFFu) == (e & 0xFFFFu) || (x >> 16) == (e >> 16);
+    }
+
+    __device__ __forceinline__ void unpack(const Raw& x, char* buf, int tok) const {
+        if (!of_values()) {
+            const int h = part_of & 1, w0 = NS == 1 ? (part_of >> 1) * (W / 2) : 0;
 #pragma unroll
-        for (int i = 0; i < KW; ++i)
-            *reinterpret_cast<h16x8*>(buf + ((sub * 2 + h) * W + w0 + i) * kOperand + lane * 16) =
-                codes8(x.k[i]);
+            for (int i = 0; i < KW; ++i)
+                *reinterpret_cast<h16x8*>(buf + ((step_of * 2 + h) * W + w0 + i) * kOperand + lane * 16) =
+                    codes8(x.w[i]);
+            const int e = entry();
+            if (e >= 0) {
+                // scales of the value that are not finite reach the rows that see it in their score
+                float* sc = reinterpret_cast<float*>(buf + kS);
+                sc[e] = lo16<F16>(x.s[0]);
+                sc[NG * T + e] = wild(x.s[1]) ? __builtin_nanf("") : hi16<F16>(x.s[0]);
+            }
+            return;
+        }
+        // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 are within
+        uint32_t top = 0;
+        bool any_wild = false;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const float s = lo16<F16>(x.t[i]), m = hi16<F16>(x.t[i]);
+            const float v = __builtin_fabsf(__builtin_fmaf(8.0f, s, m)) + 8.0f * __builtin_fabsf(s);
+            const int t = tok + step_of * kStep + 8 * g + (r & 7);
+            const bool bad = wild(x.t[i]), out = !x.ok || t < wg_lo || t >= wg_hi;
+            any_wild = any_wild || bad || out;
+            top = max(top, bad || out ? 0u : __float_as_uint(v));
+        }
+        int b = 0;
+        if constexpr (!F16) {
+            top = row_max16(top);
+            b = clampi(15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top)), -112, 100);
+        }
+        any_wild = __any(any_wild);
+        h16x2 s2[GV][4], m2[GV][4];
+#pragma unroll
+        for (int k = 0; k < GV; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float s[2], m[2];
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    uint32_t w = x.s[8 * k + 2 * i + o];
+                    if (any_wild) {
+                        const int t = tok + step_of * kStep + 8 * g + 2 * i + o;
+                        w = wild(w) || !x.ok || t < wg_lo || t >= wg_hi ? 0u : w;
+                    }
+                    s[o] = lo16<F16>(w);
+                    m[o] = __builtin_fmaf(8.0f, s[o], hi16<F16>(w));
+                    if constexpr (!F16) {
+                        s[o] = __builtin_ldexpf(s[o], b);
+                        m[o] = __builtin_ldexpf(m[o], b);
+                    }
+                }
+                s2[k][i] = __builtin_convertvector(f32x2{s[0], s[1]}, h16x2);
+                m2[k][i] = __builtin_convertvector(f32x2{m[0], m[1]}, h16x2);
+            }
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
+            const int j = part_of * VB + i;
             u32x4 op;
-            // D == 64: blocks 2 part and 2 part + 1 of the same words
-            const bool shift = D == 64 ? part != 0 : i % 4 >= 2;
 #pragma unroll
             for (int tp = 0; tp < 4; ++tp) {
-                const uint32_t w = x.v[D == 64 ? tp : tp * (VB / 4) + i / 4];
-                op[tp] = centred(shift ? w >> 8 : w, i & 1);
+                // D == 64: blocks 2 part and 2 part + 1 of the same words
+                const uint32_t w = x.w[tp] >> (D == 64 ? 8 * part_of + 4 * i : 4 * i);
+                const h16x2 c = __builtin_bit_cast(h16x2, centred(w));
+                op[tp] = __builtin_bit_cast(
+                    uint32_t, __builtin_elementwise_fma(c, s2[16 * i / G][tp], m2[16 * i / G][tp]));
             }
-            *reinterpret_cast<u32x4*>(buf + kV + (sub * NJ + part * VB + i) * kOperand + lane * 16) = op;
+            *reinterpret_cast<u32x4*>(buf + kV + (step_of * NJ + j) * kOperand + lane * 16) = op;
         }
-        float* sc = reinterpret_cast<float*>(buf + kS);
+        if (part_of == 0 && r == 0)
+            *reinterpret_cast<f32x2*>(buf + kB + 8 * (step_of * 4 + g)) =
+                f32x2{(float)b, x.ok ? 1.0f : 0.0f};
+    }
+
+    // 32 tokens: step `sub` of a turn's operands.
+    __device__ __forceinline__ void step(const char* buf, int sub, int tok) {
+        const Src src{buf, lane, g, sub};
+        const f32x2 bo = *reinterpret_cast<const f32x2*>(buf + kB + 8 * (sub * 4 + g));
+        const float b = bo.x;
+        const bool ok = bo.y != 0.0f;
+        float x[NC][8];
+        this->scores(src, x);
+        if (!(tok >= this->full_lo && tok + kStep <= this->full_hi && __all(ok))) {
 #pragma unroll
-        for (int i = 0; i < SW; ++i) {
-            int which, group, t;
-            scale_entry(i, which, group, t);
-            if (which < 2) {
-                const float s = x.in[i] ? lo16<F16>(x.s[i]) : 0.0f, m = x.in[i] ? hi16<F16>(x.s[i]) : 0.0f;
-                sc[(2 * which * NG + group) * T + t] = s;
-                sc[((2 * which + 1) * NG + group) * T + t] = which ? __builtin_fmaf(8.0f, s, m) : m;
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[c][i] = ok && this->sees(c, tok + 8 * g + i) ? x[c][i] : -__builtin_inff();
+        }
+        float top[NC];
+        const bool raise = this->tops(x, top);
+        if (__any(raise || (!F16 && b < k2)))
+            new_reference(top, b);
+        const float up = F16 ? kUp : k2 - b + kUp;
+        const float down = F16 ? 1.0f : __builtin_amdgcn_exp2f(b - k2);
+        h16x8 ph[NC], pl[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float ref = (R[c] == -__builtin_inff() ? 0.0f : R[c]) - up;
+            float pr[8], sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[c][i], fac[c], -ref));
+                sum += pr[i];
+            }
+            l[c] = F16 ? l[c] + sum : __builtin_fmaf(sum, down, l[c]);
+            split8<F16>(pr, ph[c], pl[c]);
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const h16x8 o = src.v(j);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if constexpr (F16)
+                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, pl[c], acc[c][j], 0, 0, 0);
+                acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
             }
         }
-        if (part == 0 && r == 0)
-            reinterpret_cast<int*>(buf + kOk)[sub * 4 + g] = x.ok;
+    }
+
+    __device__ __forceinline__ void new_reference(const float (&top)[NC], float b) {
+        float fit = 1.0f;
+        if constexpr (!F16) {
+            b = __builtin_fminf(b, __shfl_xor(b, 16));
+            b = __builtin_fminf(b, __shfl_xor(b, 32));
+            b = __builtin_fminf(b, k2);
+            fit = __builtin_amdgcn_exp2f(b - k2);
+            k2 = b;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float by = this->raised(c, top[c]), both = by * fit;
+            l[c] *= by;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[c][j][i] *= both;
+        }
     }
 
     __device__ __forceinline__ void run(char* lds) {
         const AttnI4& a = p.a;
         wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        step_of = NS == 2 ? (wave & 3) >> 1 : 0;
+        part_of = NS == 2 ? wave & 1 : wave & 3;
         const Place at(p);
         head = at.head;
         const Seq sq = seq_of(a, at.seq);
-        const int rows = sq.n * p.share, tile = at.tile * 16 * NC * kWaves, first = tile + wave * 16 * NC;
+        const int rows = sq.n * (int)p.share.d, tile = at.tile * 16 * NC * kRowWaves;
+        const int first = tile + wave * 16 * NC;
         if (tile >= rows)
             return;
         table = a.table + (int64_t)at.seq * a.ldt;
-        this->range(sq, tile, 16 * NC * kWaves, rows, wg_lo, wg_hi);
-        this->load_q(sq, first, rows);
+        this->range(sq, tile, 16 * NC * kRowWaves, rows, wg_lo, wg_hi);
+        this->range(sq, first, 16 * NC, rows, lo, hi);
         int b0, b1;
-        split_blocks(wg_lo, wg_hi, at.split, p.splits, T / 8, b0, b1);
+        split_blocks(wg_lo, wg_hi, at.split, p.by_splits, T / 8, b0, b1);
+        Raw x;
+        Walk wc, ws;
         if (b0 < b1) {
-            const int bpp = p.bpp;
-            Walks w;
-            w.k = Walk(b0 + 4 * step_of() + (r >> 2), T / 8, bpp);
-            w.v = Walk(b0 + 4 * step_of() + g, T / 8, bpp);
-#pragma unroll
-            for (int i = 0; i < SW; ++i) {
-                int which, group, t;
-                scale_entry(i, which, group, t);
-                w.s[i] = Walk(b0 + t / 8, T / 8, bpp);
-            }
-            auto on = [&] {
-                w.k.step(bpp);
-                w.v.step(bpp);
-#pragma unroll
-                for (int i = 0; i < SW; ++i)
-                    w.s[i].step(bpp);
-            };
-            Raw x = load(w, b0 * 8);
-            on();
-            unpack(x, lds);
+            start(b0, wc, ws);
+            x = load(wc, ws, b0 * 8);
+        }
+        this->load_q(sq, first, rows);
+        k2 = F16 ? 0.0f : 200.0f;
+        if (b0 < b1) {
+            const int bpp = (int)p.bpp.d;
+            unpack(x, lds, b0 * 8);
             if (b0 + T / 8 < b1) {
-                x = load(w, b0 * 8 + T);
-                on();
+                wc.step(bpp);
+                ws.step(bpp);
+                x = load(wc, ws, b0 * 8 + T);
             }
             int turn = 0;
             for (int b = b0; b < b1; b += T / 8, turn ^= 1) {
                 __syncthreads();        // this turn's operands are there, the last turn's are used up
                 if (b + T / 8 < b1) {
-                    unpack(x, lds + (turn ^ 1) * kBuffer);
+                    unpack(x, lds + (turn ^ 1) * kBuffer, b * 8 + T);
                     if (b + 2 * (T / 8) < b1) {
-                        x = load(w, b * 8 + 2 * T);
-                        on();
+                        wc.step(bpp);
+                        ws.step(bpp);
+                        x = load(wc, ws, b * 8 + 2 * T);
                     }
                 }
-                const char* buf = lds + turn * kBuffer;
-#pragma unroll
+#pragma unroll 1
                 for (int sub = 0; sub < NS; ++sub) {
                     const int tok = b * 8 + sub * kStep;
-                    if (tok >= hi || tok + kStep <= lo)
-                        continue;
-                    const bool ok = reinterpret_cast<const int*>(buf + kOk)[sub * 4 + g] != 0;
-                    const Src src(buf, lane, sub);
-                    if (tok >= this->full_lo && tok + kStep <= this->full_hi && __all(ok))
-                        this->template step<false>(src, tok, true);
-                    else
-                        this->template step<true>(src, tok, ok);
+                    if (tok < hi && tok + kStep > lo)
+                        step(lds + turn * kBuffer, sub, tok);
                 }
             }
         }
         const bool whole = p.splits == 1;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            float least[NG];
-            const float sum = quarter_sum(this->l[c]);
-#pragma unroll
-            for (int k = 0; k < NG; ++k)
-                least[k] = quarter_sum(this->mb[c][k]);
+            const float sum = quarter_sum(l[c]);
             const int row = first + 16 * c + r;
             if (row >= rows)
                 continue;
@@ -961,7 +1213,11 @@ struct Rows : State<D, G, F16, NC> {
             const int64_t cell = (int64_t)at.split * a.rows * a.heads + this->cell(sq, row);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const f32x4 y = this->result(c, j, least);
+                f32x4 y = acc[c][j];
+                if constexpr (!F16)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = __builtin_ldexpf(y[i], (int)-k2);
                 if (whole)
                     put4<F16>(o + 16 * j, y, by);
                 else
@@ -969,71 +1225,85 @@ struct Rows : State<D, G, F16, NC> {
             }
             if (g == 0) {
                 if (whole)
-                    this->put_lse(sq, row, this->reference(c), sum);
+                    this->put_lse(sq, row, R[c] - kUp, sum);
                 else
-                    *reinterpret_cast<f32x2*>(p.ml + 2 * cell) = f32x2{this->reference(c), sum};
+                    *reinterpret_cast<f32x2*>(p.ml + 2 * cell) = f32x2{R[c] - kUp, sum};
             }
         }
     }
 };
 
 template <int D, int G, bool F16, int NC>
-__global__ __launch_bounds__(kThreads) void k_attn_rows(Args p) {
+__global__ __launch_bounds__(512, 2) void k_attn_rows(Args p) {
     __shared__ __align__(16) char lds[2 * Rows<D, G, F16, NC>::kBuffer];
     Rows<D, G, F16, NC> k(p);
     k.run(lds);
 }
 
-// The partial results of a row joined: a wave to a row and head.
+// The partial results of a row joined: a workgroup to a row and head.  16 bytes of a result to a
+// lane, so that a workgroup reads kThreads / (D / 4) splits at a time, and every lane has few to
+// read one after the other (128 splits of one row: 34 us with a wave to a row).
 template <int D, bool F16>
 __global__ __launch_bounds__(kThreads) void k_attn_join(Args p) {
+    constexpr int kLane = D / 4, kAt = kThreads / kLane;
+    __shared__ __align__(16) float all[kAt * D];
+    __shared__ float weight[kMaxSplits];
     const AttnI4& a = p.a;
-    const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const int64_t per = (int64_t)a.max_q * a.heads;
-    const int b = (int)(at / per);
-    if (b >= a.seqs)
-        return;
-    const int qi = (int)(at % per) / a.heads, hd = (int)(at % per) % a.heads;
+    const int64_t per = (int64_t)a.max_q * a.heads, at = blockIdx.x;
+    const int b = (int)(at / per), cell0 = (int)(at - b * per), qi = cell0 / a.heads, hd = cell0 - qi * a.heads;
     const Seq sq = seq_of(a, b);
     if (qi >= sq.n)
         return;
+    const int t = threadIdx.x, lane = t & 63;
     const int64_t row = sq.row0 + qi, cell = row * a.heads + hd, cells = (int64_t)a.rows * a.heads;
+    // every wave finds the reference and the sum; a lane has splits lane, lane + 64, ..
+    f32x2 m[kMaxSplits / 64];
     float ref = -__builtin_inff(), sum = 0.0f;
-    for (int s = lane; s < p.splits; s += 64)
-        ref = __builtin_fmaxf(ref, p.ml[2 * (s * cells + cell)]);
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 64; ++i) {
+        const int s = lane + 64 * i;
+        m[i] = f32x2{-__builtin_inff(), 0.0f};
+        if (s < p.splits)
+            m[i] = *reinterpret_cast<const f32x2*>(p.ml + 2 * (s * cells + cell));
+        ref = __builtin_fmaxf(ref, m[i].x);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1)
         ref = __builtin_fmaxf(ref, __shfl_xor(ref, d));
-    constexpr int N = D / 64;
-    float y[N] = {};
-    for (int s0 = 0; s0 < p.splits; s0 += 64) {
-        float w = 0.0f, ws = 0.0f;
-        if (s0 + lane < p.splits && ref != -__builtin_inff()) {
-            const f32x2 m = *reinterpret_cast<const f32x2*>(p.ml + 2 * ((s0 + lane) * cells + cell));
-            w = __builtin_amdgcn_exp2f(m.x - ref);
-            ws = w * m.y;
-        }
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            ws += __shfl_xor(ws, d);
-        sum += ws;
-        const int n = p.splits - s0 < 64 ? p.splits - s0 : 64;
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-            const float by = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
-            const float* z = p.part + ((int64_t)(s0 + s) * cells + cell) * D + lane;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                y[i] = __builtin_fmaf(by, z[64 * i], y[i]);
-        }
+    for (int i = 0; i < kMaxSplits / 64; ++i) {
+        const float w = ref == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[i].x - ref);
+        sum += w * m[i].y;
+        if (t < 64)
+            weight[lane + 64 * i] = w;
     }
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* o = a.out + row * a.ldo + (int64_t)hd * a.hso + lane;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        o[64 * i] = (uint16_t)pack2<F16>(y[i] * by, 0.0f);
-    if (a.lse && lane == 0)
+    for (int d = 1; d < 64; d <<= 1)
+        sum += __shfl_xor(sum, d);
+    __syncthreads();
+    f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
+    const float* z = p.part + cell * D + 4 * (t % kLane);
+#pragma unroll 4
+    for (int s = t / kLane; s < p.splits; s += kAt) {
+        const float w = weight[s];
+        const f32x4 x = *reinterpret_cast<const f32x4*>(z + s * cells * D);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = __builtin_fmaf(w, x[i], y[i]);
+    }
+    *reinterpret_cast<f32x4*>(all + 4 * t) = y;
+    __syncthreads();
+    if (t < kLane) {
+#pragma unroll
+        for (int s = 1; s < kAt; ++s) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(all + 4 * (s * kLane + t));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] += x[i];
+        }
+        put4<F16>(a.out + row * a.ldo + (int64_t)hd * a.hso + 4 * t, y, sum == 0.0f ? 0.0f : 1.0f / sum);
+    }
+    if (a.lse && t == 0)
         a.lse[cell] = lse_of(ref, sum);
 }
 
@@ -1047,21 +1317,18 @@ hipError_t launch_width(std::integral_constant<int, 256>, const Args& a, const A
 
 template <int D, int G, bool F16>
 hipError_t launch_group(const Args& a, const AttnPlan& p, hipStream_t st) {
-    const dim3 grid((unsigned)(a.units * a.tiles)), block(kThreads);
+    const dim3 grid(a.units.d * (unsigned)a.tiles), block(kThreads);
     hipError_t e;
     if (!p.by_rows)
-        e = p.cols == 1 ? launch1(k_attn_tokens<D, G, F16, 1>, grid, block, st, a)
-                        : launch1(k_attn_tokens<D, G, F16, 2>, grid, block, st, a);
-    else if (p.cols == 1)
-        e = launch1(k_attn_rows<D, G, F16, 1>, grid, block, st, a);
-    else if (D == 256 || p.cols == 2)
-        e = launch1(k_attn_rows<D, G, F16, 2>, grid, block, st, a);
+        e = launch1(k_attn_tokens<D, G, F16, 1>, grid, block, st, a);
+    else if (D == 256 || p.cols == 1)
+        e = launch1(k_attn_rows<D, G, F16, 1>, grid, dim3(512), st, a);
     else
-        e = launch1(k_attn_rows<D, G, F16, D == 256 ? 2 : 4>, grid, block, st, a);
+        e = launch1(k_attn_rows<D, G, F16, D == 256 ? 1 : 2>, grid, dim3(512), st, a);
     if (e != hipSuccess || a.splits == 1)
         return e;
-    const int64_t waves = (int64_t)a.a.seqs * a.a.max_q * a.a.heads;
-    return launch1(k_attn_join<D, F16>, dim3((unsigned)((waves + kWaves - 1) / kWaves)), block, st, a);
+    return launch1(k_attn_join<D, F16>, dim3((unsigned)((int64_t)a.a.seqs * a.a.max_q * a.a.heads)), block,
+                   st, a);
 }
 
 template <int D>

@@ -16,9 +16,9 @@ AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, i
                    int kv_heads, int dim) {
     AttnPlan p{};
     const int64_t m = max_q * (heads / kv_heads);       // rows of one sequence and cache head
-    p.by_rows = m > 32;
-    p.cols = m <= 16 || (p.by_rows && m <= 64) ? 1 : m <= 128 || dim == 256 ? 2 : 4;
-    const int64_t tile = 16 * p.cols * (p.by_rows ? attn::kWaves : 1);
+    p.by_rows = m > 64;
+    p.cols = !p.by_rows || m <= 128 || dim == 256 ? 1 : 2;
+    const int64_t tile = 16 * p.cols * (p.by_rows ? 8 : 1);
     p.tiles = (int)((m + tile - 1) / tile);
     const int64_t base = seqs * kv_heads * p.tiles;
     // four workgroups to a compute unit, and 256 tokens or more to a workgroup
@@ -28,6 +28,7 @@ AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, i
     const int64_t cell = rows * heads * 4 * (dim + 2);
     const int64_t room = ((int64_t)64 << 20) / (cell > 0 ? cell : 1);
     splits = splits < room ? splits : room;
+    splits = splits < attn::kMaxSplits ? splits : attn::kMaxSplits;
     p.splits = (int)(splits < 1 ? 1 : splits);
     p.ws_bytes = p.splits > 1 ? p.splits * cell : 0;
     return p;
@@ -36,11 +37,14 @@ AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, i
 hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStream_t stream) {
     attn::Args g{};
     g.a = a;
-    g.units = (int32_t)((int64_t)a.seqs * a.c.heads * p.splits);
+    using attn::Div;
+    g.units = Div::by((uint32_t)((int64_t)a.seqs * a.c.heads * p.splits));
+    g.heads = Div::by(a.c.heads);
+    g.by_splits = Div::by(p.splits);
+    g.share = Div::by(a.heads / a.c.heads);
+    g.bpp = Div::by(a.c.page_size / 8);
     g.tiles = p.tiles;
     g.splits = p.splits;
-    g.share = a.heads / a.c.heads;
-    g.bpp = a.c.page_size / 8;
     g.scale2 = a.scale * 1.44269504088896341f;
     if (p.splits > 1) {
         g.part = static_cast<float*>(a.ws);

@@ -82,10 +82,11 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  * sequence are not written.  Tokens that a row does not see have no effect on it, whatever their
  * codes and scales hold (but for the bits that much larger scales of v cost, see below).
  *
- * Sums and softmax are in binary32; q is exact but for numbers 2^-24 below the largest of
- * their row, exp(score_t - lse) * (scale of v_t) to half a step of binary16 (2^-12; in the _f16 calls
- * 2^-21), and where it is 2^-21 of a sequence's largest or less, absolutely.  Scales of v are
- * at most 2^100 in size.  A NaN or an infinity in a row of q makes every value
+ * Scores, softmax and sums are in binary32; q is exact but for numbers 2^-24 below the largest of
+ * their row.  Before the product with the values, exp(score_t - lse) is held to half a step of
+ * binary16 (2^-12 relative; in the _f16 calls 2^-21), and v_t to about a step of it where a call has
+ * many rows.  Values of v that are 2^-16 of the largest of their sequence and head or less lose
+ * further bits; their scales are at most 2^100.  A NaN or an infinity in a row of q makes every value
  * of that row and head NaN, one in the scales of a token does not reach rows that do not see it.
  * The same call gives the same bits.
  *
