@@ -825,7 +825,8 @@ class KvI4:
             raise ValueError("KvI4: what belongs to one page and head is not contiguous")
         self.k, self.v, self.ks, self.vs = k, v, ks, vs
         self.pages, self.heads, self.page_size, self.dim, self.group = pages, heads, size, dim, group
-        self.dtype, self.device = ks.dtype, k.device
+        self.dtype, self.device, self.index = ks.dtype, k.device, k.get_device()
+        self.scale = dim ** -0.5        # of scores, where a call gives none
         self.struct = _KvI4(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.stride(0),
                             k.stride(1), ks.stride(0), ks.stride(1), pages, size, heads, dim, group)
         self.address = ctypes.addressof(self.struct)
@@ -841,59 +842,63 @@ def _refuse_rows(fn: str, cache, *arrays) -> None:
             raise ValueError(f"{fn}: {arg} is {tuple(t.shape)}, not {(tokens, heads, cache.dim)}")
         if t.stride(2) != 1:
             raise ValueError(f"{fn}: the last dimension of {arg} is not contiguous")
-        if t.device != cache.device:
+        if t.get_device() != cache.index:
             raise ValueError(f"{fn}: {arg} is on {t.device}, the cache on {cache.device}")
 
 
 def _on_current(fn: str, cache, stream):
     """The stream of a call, for a cache on torch's current device."""
     stream = _stream(stream)
-    if cache.device.index != (_raw_device() if _raw_device else cache.device.index):
+    if _raw_device is None:
+        _current_stream()
+    if cache.index != _raw_device():
         raise ValueError(f"{fn}: the cache is on {cache.device}, which is not the current device")
     return stream
 
 
-def _kv_call(name, type_, k, v, slots, cache, stream, write):
-    lib, dtype = _L(), _f16 if type_ else _bf16
-    if cache.dtype is not dtype:
-        raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
-    tokens, heads = slots.numel(), cache.heads
-    shape = (tokens, heads, cache.dim)
-    if not (slots.dtype is _i32 and slots.is_contiguous()):
+def _kv_call(name, dtype, k, v, slots, cache, stream, write):
+    fn = getattr(_lib or _L(), name)
+    tokens, index = slots.numel(), cache.index
+    shape, ks, vs = (tokens, cache.heads, cache.dim), k.stride(), v.stride()
+    if not (cache.dtype is dtype and k.dtype is dtype and v.dtype is dtype and slots.dtype is _i32
+            and k.shape == shape and v.shape == shape and ks[2] == 1 and vs[2] == 1
+            and slots.is_contiguous() and k.get_device() == v.get_device() == slots.get_device() == index):
+        if cache.dtype is not dtype:
+            raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
         _refuse(name, ("slots", slots, _i32, 0))
-    ks, vs = k.stride(), v.stride()
-    if not (k.dtype is dtype and v.dtype is dtype and k.shape == shape and v.shape == shape
-            and ks[2] == 1 and vs[2] == 1 and k.device == v.device == slots.device == cache.device):
-        _refuse_rows(name, cache, ("k", k, tokens, heads), ("v", v, tokens, heads))
+        _refuse_rows(name, cache, ("k", k, tokens, cache.heads), ("v", v, tokens, cache.heads))
         raise ValueError(f"{name}: slots is on {slots.device}, the cache on {cache.device}")
     stream = _on_current(name, cache, stream)
-    rows = (k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1])
     if write:
-        _check(name, getattr(lib, name)(*rows, slots.data_ptr(), tokens, cache.address, stream))
+        status = fn(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), tokens,
+                    cache.address, stream)
     else:
-        _check(name, getattr(lib, name)(cache.address, slots.data_ptr(), tokens, *rows, stream))
+        status = fn(cache.address, slots.data_ptr(), tokens, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+                    vs[1], stream)
+    if status:
+        _check(name, status)
 
 
 def bq_kv_write_i4(k, v, slots, cache, stream=None) -> None:
     """k, v (tokens, heads, dim) torch.bfloat16 -> the cache's slots (tokens); a slot outside the
     cache (-1) leaves its token out.  The slots of a call differ."""
-    _kv_call("bq_kv_write_i4", False, k, v, slots, cache, stream, True)
+    _kv_call("bq_kv_write_i4", _bf16, k, v, slots, cache, stream, True)
 
 
 def bq_kv_write_i4_f16(k, v, slots, cache, stream=None) -> None:
     """bq_kv_write_i4 on IEEE binary16 rows and scales."""
-    _kv_call("bq_kv_write_i4_f16", True, k, v, slots, cache, stream, True)
+    _kv_call("bq_kv_write_i4_f16", _f16, k, v, slots, cache, stream, True)
 
 
 def bq_kv_read_i4(cache, slots, k, v, stream=None) -> None:
     """The cache's slots (tokens) -> k, v (tokens, heads, dim) torch.bfloat16; zeros for a slot
     outside the cache."""
-    _kv_call("bq_kv_read_i4", False, k, v, slots, cache, stream, False)
+    _kv_call("bq_kv_read_i4", _bf16, k, v, slots, cache, stream, False)
 
 
 def bq_kv_read_i4_f16(cache, slots, k, v, stream=None) -> None:
     """bq_kv_read_i4 with IEEE binary16 scales and rows."""
-    _kv_call("bq_kv_read_i4_f16", True, k, v, slots, cache, stream, False)
+    _kv_call("bq_kv_read_i4_f16", _f16, k, v, slots, cache, stream, False)
 
 
 def bq_attn_i4_ws_bytes(seqs: int, rows: int, max_q: int, max_len: int, heads: int, kv_heads: int,
@@ -902,27 +907,37 @@ def bq_attn_i4_ws_bytes(seqs: int, rows: int, max_q: int, max_len: int, heads: i
     return _L().bq_attn_i4_ws_bytes(seqs, rows, max_q, max_len, heads, kv_heads, dim)
 
 
-def _attn_i4(name, type_, q, cache, table, lens, out, starts, max_q, max_len, causal, window, scale,
+def _attn_i4(name, dtype, q, cache, table, lens, out, starts, max_q, max_len, causal, window, scale,
              lse, ws, stream):
-    lib, i32, dtype = _L(), _i32, _f16 if type_ else _bf16
-    if cache.dtype is not dtype:
-        raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
-    shape, (seqs, cols), t_strides = q.shape, table.shape, table.stride()
-    rows, heads = shape[0], shape[1]
+    fn, i32, index = getattr(_lib or _L(), name), _i32, cache.index
+    shape, (seqs, cols), (ldt, one) = q.shape, table.shape, table.stride()
+    rows, heads, dim = shape
     qs, os_ = q.stride(), out.stride()
+    lse_at = ws_at = starts_at = None
+    ws_bytes = 0
+    fits = (q.dtype is dtype and out.dtype is dtype and cache.dtype is dtype and dim == cache.dim
+            and out.shape == shape and qs[2] == 1 and os_[2] == 1 and table.dtype is i32
+            and lens.dtype is i32 and (one == 1 or cols < 2) and lens.is_contiguous()
+            and lens.numel() == seqs and q.get_device() == index and out.get_device() == index
+            and table.get_device() == index and lens.get_device() == index)
     if starts is None:
         max_q = 1
-    elif max_q is None:
-        raise ValueError(f"{name}: max_q is needed beside starts")
-    if not (q.dtype is dtype and out.dtype is dtype and shape[2] == cache.dim and out.shape == shape
-            and qs[2] == 1 and os_[2] == 1 and table.dtype is i32 and lens.dtype is i32
-            and (t_strides[1] == 1 or cols < 2) and lens.is_contiguous() and lens.numel() == seqs
-            and (starts is None or starts.dtype is i32 and starts.is_contiguous()
-                 and starts.numel() == seqs + 1 and starts.device == cache.device)
-            and (lse is None or lse.dtype is _f32 and lse.is_contiguous()
-                 and lse.numel() == rows * heads and lse.device == cache.device)
-            and (ws is None or ws.is_contiguous() and ws.device == cache.device)
-            and q.device == out.device == table.device == lens.device == cache.device):
+    else:
+        if max_q is None:
+            raise ValueError(f"{name}: max_q is needed beside starts")
+        fits = (fits and starts.dtype is i32 and starts.is_contiguous() and starts.numel() == seqs + 1
+                and starts.get_device() == index)
+        starts_at = starts.data_ptr()
+    if lse is not None:
+        fits = (fits and lse.dtype is _f32 and lse.is_contiguous() and lse.numel() == rows * heads
+                and lse.get_device() == index)
+        lse_at = lse.data_ptr()
+    if ws is not None:
+        fits = fits and ws.is_contiguous() and ws.get_device() == index
+        ws_at, ws_bytes = ws.data_ptr(), ws.nbytes
+    if not fits:
+        if cache.dtype is not dtype:
+            raise TypeError(f"{name}: the cache holds {cache.dtype}, not {dtype}")
         _refuse_rows(name, cache, ("q", q, rows, heads), ("out", out, rows, heads))
         _refuse(name, ("lens", lens, i32, seqs), ("starts", 0 if starts is None else starts, i32, seqs + 1),
                 ("lse", 0 if lse is None else lse, _f32, rows * heads))
@@ -931,14 +946,14 @@ def _attn_i4(name, type_, q, cache, table, lens, out, starts, max_q, max_len, ca
         raise ValueError(f"{name}: table, lens, starts, lse or ws has another length, layout or device "
                          f"than q {tuple(shape)} and table {(seqs, cols)} ask for")
     if scale is None:
-        scale = cache.dim ** -0.5
+        scale = cache.scale
     stream = _on_current(name, cache, stream)
-    _check(name, getattr(lib, name)(
-        q.data_ptr(), qs[0], qs[1], cache.address, table.data_ptr(), t_strides[0] if seqs > 1 else cols,
-        cols, lens.data_ptr(), None if starts is None else starts.data_ptr(), seqs, rows, max_q,
-        cols * cache.page_size if max_len is None else max_len, heads, causal, window, scale,
-        out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), stream))
+    status = fn(q.data_ptr(), qs[0], qs[1], cache.address, table.data_ptr(), ldt if seqs > 1 else cols,
+                cols, lens.data_ptr(), starts_at, seqs, rows, max_q,
+                cols * cache.page_size if max_len is None else max_len, heads, causal, window, scale,
+                out.data_ptr(), os_[0], os_[1], lse_at, ws_at, ws_bytes, stream)
+    if status:
+        _check(name, status)
 
 
 def bq_attn_i4(q, cache, table, lens, out, starts=None, max_q: int | None = None,
@@ -952,7 +967,7 @@ def bq_attn_i4(q, cache, table, lens, out, starts=None, max_q: int | None = None
     max_q of them; None: row b alone.  max_len: at least every length (None: all that a row of the
     table has room for).  window: a row sees that many tokens at most, 0 all.  scale: dim ** -0.5
     where left out.  ws: scratch of at least bq_attn_i4_ws_bytes bytes, or None where that is 0."""
-    _attn_i4("bq_attn_i4", False, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
+    _attn_i4("bq_attn_i4", _bf16, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
              scale, lse, ws, stream)
 
 
@@ -960,7 +975,7 @@ def bq_attn_i4_f16(q, cache, table, lens, out, starts=None, max_q: int | None = 
                    max_len: int | None = None, causal: bool = True, window: int = 0,
                    scale: float | None = None, lse=None, ws=None, stream=None) -> None:
     """bq_attn_i4 on IEEE binary16 q, scales and out."""
-    _attn_i4("bq_attn_i4_f16", True, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
+    _attn_i4("bq_attn_i4_f16", _f16, q, cache, table, lens, out, starts, max_q, max_len, causal, window,
              scale, lse, ws, stream)
 
 

@@ -1488,13 +1488,13 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
     if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(lse, 4))
         return BQ_ERR_ALIGN;
     const bq::AttnPlan plan =
-        bq::attn_plan(seqs, rows, starts ? max_q : 1, max_len, heads, c.heads, c.dim);
+        bq::attn_plan(seqs, rows, starts ? max_q : 1, max_len, heads, c.heads, c.dim, c.group);
     if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes))
         return BQ_ERR_SCRATCH;
     if (plan.ws_bytes > 0 && !aligned(ws, 16))
         return BQ_ERR_ALIGN;
     if (seqs * c.heads * plan.tiles * plan.splits >= (int64_t)1 << 24 ||
-        (plan.splits > 1 && seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 24))
+        (plan.ws_bytes > 0 && seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 24))
         return BQ_ERR_SIZE;
     ins[4] = rows_span(q, rows, ldq, heads, hsq, c.dim);
     ins[5] = span(table, extent(seqs, table_cols, ldt, 4));
@@ -1582,7 +1582,7 @@ int64_t bq_attn_i4_ws_bytes(int64_t seqs, int64_t rows, int64_t max_q, int64_t m
         return -1;
     if (seqs == 0 || rows == 0 || max_q == 0)
         return 0;
-    return bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim).ws_bytes;
+    return bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim, 64).ws_bytes;
 }
 
 // ---- E4M3 128-block codec ------------------------------------------------------------------

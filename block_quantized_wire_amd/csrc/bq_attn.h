@@ -45,6 +45,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kStep = 32;           // tokens of a step
 constexpr int kMaxSplits = 256;     // of the tokens of a sequence
+constexpr int kMaxDealt = 256;      // sequences whose turns are dealt out
 constexpr float kRaise = 8.0f;      // a score may pass R by this, in powers of two
 
 // Division of n < 2^27 by a d known to the host: with 2^(p - 27) >= d and mul = ceil(2^p / d),
@@ -70,9 +71,13 @@ struct Args {
     Div share;          // heads of q to one of the cache
     Div bpp;            // blocks of 8 tokens to a page
     int32_t tiles, splits;
+    int32_t dealt;      // workgroups that share all turns, or 0: one to a unit
     float scale2;       // scale * log2(e)
-    float* part;        // partial results [splits][rows][heads][D], relative to their R
-    float* ml;          // [splits][rows][heads][2]: R, sum of p
+    // partial results, relative to their R, and (R, sum of p): [splits][rows][heads][D], or where
+    // the turns are dealt out [workgroup][2][16][D]
+    float* part;
+    float* ml;
+    int32_t* found;     // where turns are dealt out: [kMaxDealt][2] turns, turns up to there; all of them
 };
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
@@ -356,6 +361,8 @@ struct State {
                     x[c][i] = __builtin_fmaf(m[i], qs[c][k],
                                              k == 0 ? s[i] * b : __builtin_fmaf(s[i], b, x[c][i]));
                 }
+            if constexpr (NG > 2)       // or all groups' scales are held at once, and registers spill
+                __builtin_amdgcn_sched_barrier(0);
         });
     }
     // Whether row c sees token t of a page that is there.
@@ -445,6 +452,36 @@ __device__ __forceinline__ void split_blocks(int lo, int hi, int split, const Di
     b1 = b0 + per < first + n ? b0 + per : first + n;
 }
 
+// Turns of 128 tokens of sequence b, over the tokens that its rows see.
+constexpr int kTurn = 16;       // blocks of 8 tokens
+__device__ __forceinline__ int turns_of(const AttnI4& a, int b) {
+    const Seq s = seq_of(a, b);
+    const int first = s.len - s.n + 1 - a.window;       // the first row's first token, under a window
+    const int lo = a.window > 0 && first > 0 ? first : 0;
+    const int blocks = (s.len + 7) / 8 - lo / 32 * 4;
+    return s.n > 0 && blocks > 0 ? (blocks + kTurn - 1) / kTurn : 0;
+}
+
+// `total` turns dealt out to `groups` workgroups, each one a run of them.
+struct Deal {
+    int each, more;     // the first `more` workgroups have one more
+    __device__ __forceinline__ Deal(int total, int groups)
+        : each((int)((uint32_t)total / (uint32_t)groups)), more(total - each * groups) {}
+    __device__ __forceinline__ int first(int w) const { return w * each + (w < more ? w : more); }
+    // the workgroup that has turn t
+    __device__ __forceinline__ int of(int t) const {
+        const int high = more * (each + 1);
+        return t < high ? (int)((uint32_t)t / (uint32_t)(each + 1))
+                        : more + (int)((uint32_t)(t - high) / (uint32_t)each);
+    }
+};
+
+// Workgroups of few rows that a compute unit holds.
+// Their registers decide: a spilled one would be loaded behind the ring and drain it.
+constexpr int tokens_groups(int dim, int group, bool dealt) {
+    return dim == 64 ? (dealt ? 3 : 4) : dim == 128 && group >= 64 ? 3 : dim == 256 && group == 32 ? 1 : 2;
+}
+
 // ---- few rows: the waves of a workgroup share its tokens --------------------------------------
 //
 // Each wave takes every fourth step of the workgroup's tokens and keeps to itself: a ring of
@@ -453,8 +490,14 @@ __device__ __forceinline__ void split_blocks(int lo, int hi, int split, const Di
 // results meet.
 // Chunks of 16 bytes are permuted within a block so that neither operand's reads meet a
 // bank conflict.  Scales: one word or a few to a lane of a quarter wave, broadcast as DPP operands.
-template <int D, int G, bool F16, int NC>
-struct Tokens : State<D, G, F16, NC> {
+//
+// Sequences of a batch differ in length, which only the device knows.  So the turns of all of them
+// (one after the other, tile by tile and head by head) are dealt out evenly to as many workgroups
+// as the card holds at once, each of which takes its run of turns through one unit (a sequence,
+// tile and head) or several; only units that workgroups share leave partial results.
+template <int D, int G, bool F16, bool Dealt>
+struct Tokens : State<D, G, F16, 1> {
+    static constexpr int NC = 1;
     using S = State<D, G, F16, NC>;
     using S::W, S::NJ, S::NG, S::p, S::lane, S::r, S::g, S::head, S::lo, S::hi;
     using S::acc, S::R, S::l, S::fac;
@@ -464,8 +507,8 @@ struct Tokens : State<D, G, F16, NC> {
     static constexpr int kLoads = 2 * kJ + NG;
     static constexpr int kV = 16 * D, kS = 32 * D, kSlot = 32 * D + 256 * NG;
     // workgroups that a compute unit holds, and the steps that leave room for them
-    static constexpr int kGroups = NC == 1 && D <= 128 ? 3 : 2;
-    static constexpr int kMost = 160 * 1024 / (kGroups * kWaves * kSlot);
+    static constexpr int kGroups = tokens_groups(D, G, Dealt);
+    static constexpr int kMost = (kGroups == 1 ? 128 : 160 / kGroups - 4) * 1024 / (kWaves * kSlot);
     static constexpr int Depth = kMost > 4 ? 4 : kMost;
     static_assert(Depth >= 2, "a step is used while the next is loaded");
     static constexpr int kJoin = (kWaves * 16 * (D + 4) + kWaves * 16 * 2) * 4;
@@ -485,11 +528,18 @@ struct Tokens : State<D, G, F16, NC> {
     }
 
     struct Src {
-        uint32_t kw[2][W], vw[NJ];
+        const char* slot;
+        uint32_t kw[2][W];
         float ss[NG], sm[NG], s_max;
 
         __device__ __forceinline__ h16x8 k(int h, int w) const { return codes8(kw[h][w]); }
-        __device__ __forceinline__ h16x8 v(int j) const {
+        // Codes of values, read when the scores are done: registers are short before that.
+        __device__ __forceinline__ void load_v(uint32_t (&vw)[NJ], int r, int g) const {
+#pragma unroll
+            for (int i = 0; i < NJ / 4; ++i)
+                put(vw + 4 * i, slot + kV + g * 4 * D + 16 * v_slot(r * (NJ / 4) + i));
+        }
+        static __device__ __forceinline__ h16x8 v(const uint32_t (&vw)[NJ], int j) {
             u32x4 op;
 #pragma unroll
             for (int tp = 0; tp < 4; ++tp) {
@@ -514,7 +564,7 @@ struct Tokens : State<D, G, F16, NC> {
             eight<8 * NG + 8 * K>(s, m, std::make_integer_sequence<int, 8>{});
         }
         // `in`: some row sees the token whose words this lane has.
-        __device__ __forceinline__ Src(const char* slot, bool in, int r, int g) : s_max(0.0f) {
+        __device__ __forceinline__ Src(const char* at, bool in, int r, int g) : slot(at), s_max(0.0f) {
             const uint32_t b = (uint32_t)r >> 2;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -531,9 +581,6 @@ struct Tokens : State<D, G, F16, NC> {
                                                16 * k_slot(row * (D / 32) + g * (W / 4) + i, b));
                 }
             }
-#pragma unroll
-            for (int i = 0; i < NJ / 4; ++i)
-                put(vw + 4 * i, slot + kV + g * 4 * D + 16 * v_slot(r * (NJ / 4) + i));
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int e = 16 * i + r, which = e >> 3;       // groups of keys, then of values
@@ -568,16 +615,24 @@ struct Tokens : State<D, G, F16, NC> {
         float x[NC][8];
         this->scores(src, x);
         if (mask) {
+            // the scales as other values than those used below, or the compiler takes the broadcasts
+            // of all groups in front of this branch and spills
+            Src apart = src;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+                asm("" : "+v"(apart.ss[i]), "+v"(apart.sm[i]));
             float bad[8];
             S::template unroll<NG>([&](auto gi) {
                 constexpr int k = decltype(gi)::value;
                 float s[8], m[8];
-                src.template v_scales<k>(s, m);
+                apart.template v_scales<k>(s, m);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float z = s[i] * 0.0f + m[i] * 0.0f;      // 0, or NaN
                     bad[i] = k == 0 ? z : bad[i] + z;
                 }
+                if constexpr (NG > 2)
+                    __builtin_amdgcn_sched_barrier(0);
             });
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -589,6 +644,8 @@ struct Tokens : State<D, G, F16, NC> {
         const bool raise = this->tops(x, top);
         if (__any(raise || src.s_max > s_lim))
             new_reference(top, src.s_max);
+        uint32_t vw[NJ];
+        src.load_v(vw, r, g);
         float pr[NC][8];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -626,7 +683,7 @@ struct Tokens : State<D, G, F16, NC> {
             }
 #pragma unroll
             for (int j = k * (NJ / NG); j < (k + 1) * (NJ / NG); ++j) {
-                const h16x8 o = src.v(j);
+                const h16x8 o = Src::v(vw, j);
                 // -8 times the power of two of an even, of an odd block's codes
                 const uint32_t e = j & 1 ? 0x80808080u : 0x80088008u;
                 const h16x8 eight = __builtin_bit_cast(h16x8, u32x4{e, e, e, e});
@@ -640,6 +697,8 @@ struct Tokens : State<D, G, F16, NC> {
                     acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
                 }
             }
+            if constexpr (NG > 2)
+                __builtin_amdgcn_sched_barrier(0);
         });
     }
 
@@ -767,21 +826,24 @@ struct Tokens : State<D, G, F16, NC> {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
-    __device__ __forceinline__ void run(char* lds) {
+    // Turns [t0, t0 + n) of a unit; its result, or a partial one into `slot`.
+    __device__ __forceinline__ void segment(char* lds, int seq, int cache_head, int tile, int t0, int n,
+                                            int slot) {
         const AttnI4& a = p.a;
         const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        const Place at(p);
-        head = at.head;
-        const Seq sq = seq_of(a, at.seq);
-        const int rows = sq.n * (int)p.share.d, first = at.tile * 16 * NC;
+        head = cache_head;
+        const Seq sq = seq_of(a, seq);
+        const int rows = sq.n * (int)p.share.d, first = tile * 16;
         if (first >= rows)
             return;
-        table = a.table + (int64_t)at.seq * a.ldt;
+        table = a.table + (int64_t)seq * a.ldt;
         char* ring = lds + wave * Depth * kSlot;
-        int from, to;
-        this->range(sq, first, 16 * NC, rows, lo, hi);
-        split_blocks(lo, hi, at.split, p.by_splits, 4 * kWaves, from, to);
-        begin(ring, from + 4 * wave, to);
+        int from;
+        this->range(sq, 0, rows, rows, from, hi);
+        from = from / 32 * 4 + t0 * kTurn;
+        const int to = from + n * kTurn, end = (hi + 7) / 8;
+        begin(ring, from + 4 * wave, to < end ? to : end);
+        this->range(sq, first, 16, rows, lo, hi);
         this->load_q(sq, first, rows);
         k2 = 0.0f;
         s_lim = 0.0f;
@@ -791,7 +853,7 @@ struct Tokens : State<D, G, F16, NC> {
             for (int k = 0; k < NG; ++k)
                 mb[c][k] = 0.0f;
         walk(ring);
-        const bool whole = p.splits == 1;
+        const bool whole = slot < 0;
         // the waves' parts, where the rings were: [wave][row][D + 4], then (R, sum)
         constexpr int LD = D + 4;
         float* all = reinterpret_cast<float*>(lds);
@@ -827,7 +889,7 @@ struct Tokens : State<D, G, F16, NC> {
             if (row >= rows)
                 continue;
             const float by = whole ? (total == 0.0f ? 0.0f : 1.0f / total) : 1.0f;
-            const int64_t cell = (int64_t)at.split * a.rows * a.heads + this->cell(sq, row);
+            const int64_t cell = 16 * (int64_t)slot + mine;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
                 f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
@@ -851,14 +913,85 @@ struct Tokens : State<D, G, F16, NC> {
                     *reinterpret_cast<f32x2*>(p.ml + 2 * cell) = f32x2{ref, total};
             }
         }
+        __syncthreads();        // the rings may be filled again
+    }
+
+    __device__ __forceinline__ void run(char* lds, int* turns) {
+        const AttnI4& a = p.a;
+        if constexpr (!Dealt) {
+            const Place at(p);
+            segment(lds, at.seq, at.head, at.tile, 0, 1 << 23, -1);
+            return;
+        }
+        // every wave adds up the sequences' turns: lane i finds those of i, i + 64, ..; one of them
+        // leaves in LDS how many each has, and all up to its end
+        const int units = a.c.heads * p.tiles;
+        int past[kMaxDealt / 64], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxDealt / 64; ++i) {
+            const int b = 64 * i + lane;
+            past[i] = 0;
+            if (64 * i < a.seqs) {
+                const int n = b < a.seqs ? turns_of(a, b) : 0;
+                int v = n;
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) {
+                    const int u = __shfl_up(v, d);
+                    v += lane >= d ? u : 0;
+                }
+                past[i] = sum + v;
+                sum += __builtin_amdgcn_readlane(v, 63);
+                if (threadIdx.x < 64) {
+                    turns[b] = n;
+                    turns[kMaxDealt + b] = past[i];
+                    if (blockIdx.x == 0)        // for those who join
+                        *reinterpret_cast<u32x2*>(p.found + 2 * b) = u32x2{(uint32_t)n, (uint32_t)past[i]};
+                }
+            }
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            p.found[2 * kMaxDealt] = sum;
+        const Deal deal(sum * units, p.dealt);
+        const int w = (int)blockIdx.x;
+        int at = deal.first(w);
+        const int end = deal.first(w + 1);
+        if (at >= end)
+            return;
+        int b = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxDealt / 64; ++i)
+            if (64 * i < a.seqs)
+                b += __popcll(__ballot(64 * i + lane < a.seqs && past[i] * units <= at));
+        __syncthreads();
+        int count = __builtin_amdgcn_readfirstlane(turns[b]);
+        const int before = __builtin_amdgcn_readfirstlane(turns[kMaxDealt + b]) - count;
+        int unit = (int)((uint32_t)(at - before * units) / (uint32_t)count);
+        int t = at - before * units - unit * count;
+        while (true) {
+            const int take = end - at < count - t ? end - at : count - t;
+            const int tile = p.heads.div(unit);
+            segment(lds, b, unit - tile * a.c.heads, tile, t, take,
+                    take == count ? -1 : 2 * w + (t == 0 ? 1 : 0));
+            at += take;
+            if (at >= end)
+                break;
+            t = 0;
+            if (++unit == units) {
+                unit = 0;
+                do
+                    count = __builtin_amdgcn_readfirstlane(turns[++b]);
+                while (count == 0);
+            }
+        }
     }
 };
 
-template <int D, int G, bool F16, int NC>
-__global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, NC>::kGroups)) void k_attn_tokens(Args p) {
-    __shared__ __align__(16) char lds[Tokens<D, G, F16, NC>::kLds];
-    Tokens<D, G, F16, NC> k(p);
-    k.run(lds);
+template <int D, int G, bool F16, bool Dealt>
+__global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void k_attn_tokens(Args p) {
+    __shared__ __align__(16) char lds[Tokens<D, G, F16, Dealt>::kLds];
+    __shared__ int turns[Dealt ? 2 * kMaxDealt : 1];
+    Tokens<D, G, F16, Dealt> k(p);
+    k.run(lds, turns);
 }
 
 // ---- many rows: the waves share the tokens' operands ------------------------------------------
@@ -1241,70 +1374,88 @@ __global__ __launch_bounds__(512, 2) void k_attn_rows(Args p) {
 }
 
 // The partial results of a row joined: a workgroup to a row and head.  16 bytes of a result to a
-// lane, so that a workgroup reads kThreads / (D / 4) splits at a time, and every lane has few to
-// read one after the other (128 splits of one row: 34 us with a wave to a row).
+// lane, so that a workgroup reads kThreads / (D / 4) partial results at a time, each beside its
+// reference, and every lane has few to read one after the other (128 of one row: 34 us with a wave
+// to a row, 5 so).
 template <int D, bool F16>
 __global__ __launch_bounds__(kThreads) void k_attn_join(Args p) {
     constexpr int kLane = D / 4, kAt = kThreads / kLane;
     __shared__ __align__(16) float all[kAt * D];
-    __shared__ float weight[kMaxSplits];
+    __shared__ float sums[kAt], refs[kAt];
     const AttnI4& a = p.a;
     const int64_t per = (int64_t)a.max_q * a.heads, at = blockIdx.x;
     const int b = (int)(at / per), cell0 = (int)(at - b * per), qi = cell0 / a.heads, hd = cell0 - qi * a.heads;
     const Seq sq = seq_of(a, b);
     if (qi >= sq.n)
         return;
-    const int t = threadIdx.x, lane = t & 63;
+    const int t = threadIdx.x;
     const int64_t row = sq.row0 + qi, cell = row * a.heads + hd, cells = (int64_t)a.rows * a.heads;
-    // every wave finds the reference and the sum; a lane has splits lane, lane + 64, ..
-    f32x2 m[kMaxSplits / 64];
-    float ref = -__builtin_inff(), sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 64; ++i) {
-        const int s = lane + 64 * i;
-        m[i] = f32x2{-__builtin_inff(), 0.0f};
-        if (s < p.splits)
-            m[i] = *reinterpret_cast<const f32x2*>(p.ml + 2 * (s * cells + cell));
-        ref = __builtin_fmaxf(ref, m[i].x);
+    // the partial results: `count` of them, the first at `from`, then at `next`, `step` apart
+    int count = p.splits;
+    int64_t from = cell, next = cell + cells, step = cells;
+    if (p.dealt) {
+        const int units = a.c.heads * p.tiles, mine = p.found[2 * b];
+        const int share = (int)p.share.d, r = qi * share + p.share.mod(hd);     // row of its cache head
+        const int first = (p.found[2 * b + 1] - mine) * units + (r / 16 * a.c.heads + p.share.div(hd)) * mine;
+        const Deal deal(p.found[2 * kMaxDealt] * units, p.dealt);
+        count = 0;
+        if (mine > 0) {
+            const int w0 = deal.of(first), w1 = deal.of(first + mine - 1);
+            if (w0 == w1)
+                return;         // the workgroup has written the result
+            count = w1 - w0 + 1;
+            from = (int64_t)(2 * w0 + 1) * 16 + r % 16;
+            next = (int64_t)(2 * w0 + 2) * 16 + r % 16;
+            step = 32;
+        }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        ref = __builtin_fmaxf(ref, __shfl_xor(ref, d));
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 64; ++i) {
-        const float w = ref == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[i].x - ref);
-        sum += w * m[i].y;
-        if (t < 64)
-            weight[lane + 64 * i] = w;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        sum += __shfl_xor(sum, d);
-    __syncthreads();
+    const float none = -__builtin_inff();
+    float ref = none, sum = 0.0f;
     f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
-    const float* z = p.part + cell * D + 4 * (t % kLane);
 #pragma unroll 4
-    for (int s = t / kLane; s < p.splits; s += kAt) {
-        const float w = weight[s];
-        const f32x4 x = *reinterpret_cast<const f32x4*>(z + s * cells * D);
+    for (int s = t / kLane; s < count; s += kAt) {
+        const int64_t at_s = s == 0 ? from : next + (s - 1) * step;
+        const f32x2 m = *reinterpret_cast<const f32x2*>(p.ml + 2 * at_s);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p.part + at_s * D + 4 * (t % kLane));
+        const float top = __builtin_fmaxf(ref, m.x);
+        // without a reference a part is 0, or a NaN
+        const float old = ref == none ? 0.0f : __builtin_amdgcn_exp2f(ref - top);
+        const float w = m.x == none ? 0.0f : __builtin_amdgcn_exp2f(m.x - top);
+        ref = top;
+        sum = __builtin_fmaf(w, m.y, sum * old);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            y[i] = __builtin_fmaf(w, x[i], y[i]);
+            y[i] = __builtin_fmaf(w, x[i], y[i] * old);
     }
     *reinterpret_cast<f32x4*>(all + 4 * t) = y;
+    if (t % kLane == 0) {
+        sums[t / kLane] = sum;
+        refs[t / kLane] = ref;
+    }
     __syncthreads();
     if (t < kLane) {
+        const float own = ref;
+#pragma unroll
+        for (int s = 0; s < kAt; ++s)
+            ref = __builtin_fmaxf(ref, refs[s]);
+        float w = own == none ? 0.0f : __builtin_amdgcn_exp2f(own - ref);
+        sum *= w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] *= w;
 #pragma unroll
         for (int s = 1; s < kAt; ++s) {
+            w = refs[s] == none ? 0.0f : __builtin_amdgcn_exp2f(refs[s] - ref);
+            sum = __builtin_fmaf(w, sums[s], sum);
             const f32x4 x = *reinterpret_cast<const f32x4*>(all + 4 * (s * kLane + t));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                y[i] += x[i];
+                y[i] = __builtin_fmaf(w, x[i], y[i]);
         }
         put4<F16>(a.out + row * a.ldo + (int64_t)hd * a.hso + 4 * t, y, sum == 0.0f ? 0.0f : 1.0f / sum);
+        if (a.lse && t == 0)
+            a.lse[cell] = lse_of(ref, sum);
     }
-    if (a.lse && t == 0)
-        a.lse[cell] = lse_of(ref, sum);
 }
 
 // One overload for each width, each in a file of its own.
@@ -1319,13 +1470,15 @@ template <int D, int G, bool F16>
 hipError_t launch_group(const Args& a, const AttnPlan& p, hipStream_t st) {
     const dim3 grid(a.units.d * (unsigned)a.tiles), block(kThreads);
     hipError_t e;
-    if (!p.by_rows)
-        e = launch1(k_attn_tokens<D, G, F16, 1>, grid, block, st, a);
+    if (a.dealt)
+        e = launch1(k_attn_tokens<D, G, F16, true>, dim3((unsigned)a.dealt), block, st, a);
+    else if (!p.by_rows)
+        e = launch1(k_attn_tokens<D, G, F16, false>, grid, block, st, a);
     else if (D == 256 || p.cols == 1)
         e = launch1(k_attn_rows<D, G, F16, 1>, grid, dim3(512), st, a);
     else
         e = launch1(k_attn_rows<D, G, F16, D == 256 ? 1 : 2>, grid, dim3(512), st, a);
-    if (e != hipSuccess || a.splits == 1)
+    if (e != hipSuccess || (a.splits == 1 && a.dealt == 0))
         return e;
     return launch1(k_attn_join<D, F16>, dim3((unsigned)((int64_t)a.a.seqs * a.a.max_q * a.a.heads)), block,
                    st, a);

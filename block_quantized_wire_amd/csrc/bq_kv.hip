@@ -7,9 +7,10 @@
 // two bf16 numbers does not overflow, and rounded to binary32 once, as a quotient.
 //
 // Both directions are streams.  Eight lanes own a token's row of one head and a wave 8
-// consecutive tokens, which in a prefill are one block of v's layout: its words come out whole.
-// Keys: a lane has dim/8 numbers that follow each other.  Values: a lane has the numbers
-// 16j + 2u and 16j + 2u + 1 of every j, so that it owns whole half-words of the block's words.
+// consecutive tokens, which in a prefill are one block of v's layout or two.  Rows go in and out in
+// runs of 128 bytes, 16 to a lane.  Keys: a lane has whole words of 8 numbers.  Values: a lane has
+// the numbers 16j + 2u and 16j + 2u + 1 of every j, so that it owns whole half-words of the
+// block's words; two tokens that share them put theirs together.
 #include <type_traits>
 
 #include "bq_device.h"
@@ -76,7 +77,9 @@ template <bool F16>
 __device__ __forceinline__ Group group_of(float lo, float hi) {
     Group g;
     g.lo = lo;
-    const float s = (float)(((double)hi - (double)lo) / 15.0);
+    // the product is within 2^-52 of the quotient, which is periodic (1/15: period 4) and so at least
+    // 1/30 of a step away from what binary32 rounds the other way, or exact
+    const float s = (float)(((double)hi - (double)lo) * (1.0 / 15.0));
     uint32_t w = pack2<F16>(s, lo);
     const bool fine = __builtin_fabsf(lo) < __builtin_inff() && __builtin_fabsf(hi) < __builtin_inff();
     if (!fine)
@@ -131,69 +134,104 @@ __device__ __forceinline__ uint32_t v_half(uint32_t place, uint32_t r, uint32_t 
            (place & 1) * 2;
 }
 
+// A row of values between the lanes' two views of it, through LDS: 16-byte chunks u and u + 8, .. as
+// they lie in memory, and pairs 16j + 2u, 16j + 2u + 1 as the cache's words want them.  Rows are
+// 16 bytes * 2 apart from a multiple of the 64 banks, so that neither view meets a conflict.
+template <int D>
+struct Turn {
+    static constexpr int kRow = 2 * D + 32;                 // bytes
+    static constexpr int kBytes = kThreads / 8 * kRow;
+    char* row;
+    uint32_t u;
+    __device__ __forceinline__ explicit Turn(char* lds)
+        : row(lds + (threadIdx.x >> 3) * kRow), u(threadIdx.x & 7) {}
+    __device__ __forceinline__ u32x4* chunk(int i) const {
+        return reinterpret_cast<u32x4*>(row + 16 * (u + 8 * i));
+    }
+    __device__ __forceinline__ uint32_t* pair(int j) const {
+        return reinterpret_cast<uint32_t*>(row + 4 * (u + 8 * j));
+    }
+    // The lanes of a row are of one wave: what they wrote is there once its LDS accesses are done.
+    static __device__ __forceinline__ void done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+};
+
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(kThreads) void k_kv_write(KvArgs p) {
-    constexpr int NW = D / 64;          // words of k to a lane
+    constexpr int NW = D / 64;          // words of k to a lane: numbers 64i + 8u ..
     constexpr int NJ = D / 16;          // pairs of v to a lane
     constexpr int NG = D / G;
+    constexpr int HW = D / 64;          // half-words of v to a number-row
+    __shared__ __align__(16) char lds[Turn<D>::kBytes];
+    const Turn<D> turn(lds);
     const uint32_t u = threadIdx.x & 7;
     for (int64_t unit = (blockIdx.x * (int64_t)kThreads + threadIdx.x) >> 3; unit < p.units;
          unit += (gridDim.x * (int64_t)kThreads) >> 3) {
         const Row r = row_of<D>(p, unit);
+        // the token beside this one, whose half of each word of v its lanes have: 8 lanes on
+        const uint32_t key = r.in ? (uint32_t)p.r.slot[r.token] : ~0u;
+        const bool paired = dpp<0x128>(key) == (key ^ 1u) && r.in;      // row_ror:8
         if (!r.in)      // the 8 lanes of a row leave together
             continue;
-        const uint16_t* k = p.r.k + r.token * p.r.ldk + r.head * p.r.hsk + u * (D / 8);
-        const uint16_t* v = p.r.v + r.token * p.r.ldv + r.head * p.r.hsv + u * 2;
-        u32x4 kw[NW];
-        uint32_t vw[NJ];
+        const uint16_t* k = p.r.k + r.token * p.r.ldk + r.head * p.r.hsk + u * 8;
+        const uint16_t* v = p.r.v + r.token * p.r.ldv + r.head * p.r.hsv + u * 8;
+        u32x4 kw[NW], vc[NW];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            kw[i] = ld16(k + 64 * i);
+            vc[i] = ld16(v + 64 * i);
+        }
 #pragma unroll
         for (int i = 0; i < NW; ++i)
-            kw[i] = ld16(k + 8 * i);
+            *turn.chunk(i) = vc[i];
+        uint8_t* c = p.c.k + r.code + (int64_t)r.place * (D / 2);
+        constexpr int PW = G >= 64 ? G / 64 : 1;        // words of a lane that share a group
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            vw[j] = *reinterpret_cast<const uint32_t*>(v + 16 * j);
-        {
-            float f[8 * NW];
+        for (int i0 = 0; i0 < NW; i0 += PW) {
+            float f[8 * PW];
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
+            for (int i = 0; i < PW; ++i) {
                 if constexpr (F16)
-                    unpack_f16x8(kw[i], f + 8 * i);
+                    unpack_f16x8(kw[i0 + i], f + 8 * i);
                 else
-                    unpack_bf16x8(kw[i], f + 8 * i);
+                    unpack_bf16x8(kw[i0 + i], f + 8 * i);
             }
             float lo = f[0], hi = f[0];
 #pragma unroll
-            for (int i = 1; i < 8 * NW; ++i) {
+            for (int i = 1; i < 8 * PW; ++i) {
                 lo = __builtin_elementwise_minimum(lo, f[i]);
                 hi = __builtin_elementwise_maximum(hi, f[i]);
             }
-            constexpr int L = G / (D / 8);      // lanes of a group
+            constexpr int L = G >= 64 ? 8 : 4;          // lanes of a group
             lanes_min_max<L>(lo, hi);
             const Group g = group_of<F16>(lo, hi);
-            uint8_t* c = p.c.k + r.code + (int64_t)r.place * (D / 2);
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
+            for (int i = 0; i < PW; ++i) {
                 uint32_t w = 0;
 #pragma unroll
                 for (int n = 0; n < 8; ++n)
                     w |= code_of(f[8 * i + n], g) << (4 * n);
                 if (!g.live)
                     w = 0;
-                const uint32_t at = u * NW + i;     // numbers 8 at .. 8 at + 7
+                const uint32_t at = 8 * (i0 + i) + u;   // numbers 8 at .. 8 at + 7
                 *reinterpret_cast<uint32_t*>(c + ((at & 3) * (D / 32) + (at >> 2)) * 4) = w;
             }
             if (u % L == 0)
-                *reinterpret_cast<uint32_t*>(p.c.ks + r.scale +
-                                             2 * ((int64_t)(u / L) * p.c.page_size + r.place)) =
-                    g.pair;
+                *reinterpret_cast<uint32_t*>(
+                    p.c.ks + r.scale +
+                    2 * ((int64_t)((64 * i0 + 8 * u) / G) * p.c.page_size + r.place)) = g.pair;
         }
-        uint32_t half[2][D / 64] = {};
+        Turn<D>::done();
+        uint32_t half[2][HW] = {};
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
             constexpr int PJ = G / 16;          // pairs of a group
-            float lo = lo16<F16>(vw[gi * PJ]), hi = lo;
+            uint32_t vw[PJ];
 #pragma unroll
-            for (int j = gi * PJ; j < (gi + 1) * PJ; ++j) {
+            for (int j = 0; j < PJ; ++j)
+                vw[j] = *turn.pair(gi * PJ + j);
+            float lo = lo16<F16>(vw[0]), hi = lo;
+#pragma unroll
+            for (int j = 0; j < PJ; ++j) {
                 const float a = lo16<F16>(vw[j]), b = hi16<F16>(vw[j]);
                 lo = __builtin_elementwise_minimum(lo, __builtin_elementwise_minimum(a, b));
                 hi = __builtin_elementwise_maximum(hi, __builtin_elementwise_maximum(a, b));
@@ -201,8 +239,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvArgs p) {
             lanes_min_max<8>(lo, hi);
             const Group g = group_of<F16>(lo, hi);
 #pragma unroll
-            for (int j = gi * PJ; j < (gi + 1) * PJ; ++j) {
-                const uint32_t a = code_of(lo16<F16>(vw[j]), g), b = code_of(hi16<F16>(vw[j]), g);
+            for (int i = 0; i < PJ; ++i) {
+                const int j = gi * PJ + i;
+                const uint32_t a = code_of(lo16<F16>(vw[i]), g), b = code_of(hi16<F16>(vw[i]), g);
                 half[0][j / 4] |= (g.live ? a : 0) << (4 * (j % 4));
                 half[1][j / 4] |= (g.live ? b : 0) << (4 * (j % 4));
             }
@@ -210,47 +249,59 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvArgs p) {
                 *reinterpret_cast<uint32_t*>(p.c.vs + r.scale +
                                              2 * ((int64_t)gi * p.c.page_size + r.place)) = g.pair;
         }
-        uint8_t* c = p.c.v + r.code;
+        uint8_t* cv = p.c.v + r.code;
+        if (paired) {
+            // the even token writes both tokens' words of number-row 2u, the odd one those of 2u + 1
+            const uint32_t odd = r.place & 1;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+            for (int hw = 0; hw < HW; ++hw) {
+                const uint32_t other = dpp<0x128>(odd ? half[0][hw] : half[1][hw]);
+                const uint32_t w = odd ? other | half[1][hw] << 16 : half[0][hw] | other << 16;
+                *reinterpret_cast<uint32_t*>(cv + v_half<D>(r.place & ~1u, 2 * u + odd, hw)) = w;
+            }
+        } else {
 #pragma unroll
-            for (int hw = 0; hw < D / 64; ++hw)
-                *reinterpret_cast<uint16_t*>(c + v_half<D>(r.place, 2 * u + b, hw)) =
-                    (uint16_t)half[b][hw];
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int hw = 0; hw < HW; ++hw)
+                    *reinterpret_cast<uint16_t*>(cv + v_half<D>(r.place, 2 * u + b, hw)) =
+                        (uint16_t)half[b][hw];
+        }
+        Turn<D>::done();
     }
 }
 
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(kThreads) void k_kv_read(KvArgs p) {
-    constexpr int NW = D / 64, NJ = D / 16;
+    constexpr int NW = D / 64, NJ = D / 16, HW = D / 64;
+    __shared__ __align__(16) char lds[Turn<D>::kBytes];
+    const Turn<D> turn(lds);
     const uint32_t u = threadIdx.x & 7;
     for (int64_t unit = (blockIdx.x * (int64_t)kThreads + threadIdx.x) >> 3; unit < p.units;
          unit += (gridDim.x * (int64_t)kThreads) >> 3) {
         const Row r = row_of<D>(p, unit);
         if (r.token >= p.r.tokens)
             continue;
-        uint16_t* ko = p.r.ko + r.token * p.r.ldk + r.head * p.r.hsk + u * (D / 8);
-        uint16_t* vo = p.r.vo + r.token * p.r.ldv + r.head * p.r.hsv + u * 2;
+        uint16_t* ko = p.r.ko + r.token * p.r.ldk + r.head * p.r.hsk + u * 8;
+        uint16_t* vo = p.r.vo + r.token * p.r.ldv + r.head * p.r.hsv + u * 8;
         if (!r.in) {
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                *reinterpret_cast<u32x4*>(ko + 8 * i) = u32x4{};
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                *reinterpret_cast<uint32_t*>(vo + 16 * j) = 0;
+            for (int i = 0; i < NW; ++i) {
+                st16(ko + 64 * i, u32x4{});
+                st16(vo + 64 * i, u32x4{});
+            }
             continue;
         }
         const uint8_t* ck = p.c.k + r.code + (int64_t)r.place * (D / 2);
         const uint8_t* cv = p.c.v + r.code;
         const uint32_t* ks = reinterpret_cast<const uint32_t*>(p.c.ks + r.scale) + r.place;
         const uint32_t* vs = reinterpret_cast<const uint32_t*>(p.c.vs + r.scale) + r.place;
-        constexpr int L = G / (D / 8);
-        const uint32_t kp = ks[(int64_t)(u / L) * p.c.page_size];
-        uint32_t kw[NW], vp[D / G], half[2][D / 64];
+        uint32_t kw[NW], kp[NW], vp[D / G], half[2][HW];
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            const uint32_t at = u * NW + i;
+            const uint32_t at = 8 * i + u;      // numbers 8 at .. 8 at + 7
             kw[i] = *reinterpret_cast<const uint32_t*>(ck + ((at & 3) * (D / 32) + (at >> 2)) * 4);
+            kp[i] = ks[(int64_t)(8 * at / G) * p.c.page_size];
         }
 #pragma unroll
         for (int g = 0; g < D / G; ++g)
@@ -258,11 +309,18 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvArgs p) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int hw = 0; hw < D / 64; ++hw)
+            for (int hw = 0; hw < HW; ++hw)
                 half[b][hw] = *reinterpret_cast<const uint16_t*>(cv + v_half<D>(r.place, 2 * u + b, hw));
-        const float s = lo16<F16>(kp), m = hi16<F16>(kp);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const float sv = lo16<F16>(vp[16 * j / G]), mv = hi16<F16>(vp[16 * j / G]);
+            const float a = (float)((half[0][j / 4] >> (4 * (j % 4))) & 15u);
+            const float b = (float)((half[1][j / 4] >> (4 * (j % 4))) & 15u);
+            *turn.pair(j) = pack2<F16>(__builtin_fmaf(a, sv, mv), __builtin_fmaf(b, sv, mv));
+        }
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
+            const float s = lo16<F16>(kp[i]), m = hi16<F16>(kp[i]);
             u32x4 w;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -270,16 +328,13 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvArgs p) {
                 w[n] = pack2<F16>(__builtin_fmaf((float)(c & 15u), s, m),
                                   __builtin_fmaf((float)((c >> 4) & 15u), s, m));
             }
-            *reinterpret_cast<u32x4*>(ko + 8 * i) = w;
+            st16(ko + 64 * i, w);
         }
+        Turn<D>::done();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const float sv = lo16<F16>(vp[16 * j / G]), mv = hi16<F16>(vp[16 * j / G]);
-            const float a = (float)((half[0][j / 4] >> (4 * (j % 4))) & 15u);
-            const float b = (float)((half[1][j / 4] >> (4 * (j % 4))) & 15u);
-            *reinterpret_cast<uint32_t*>(vo + 16 * j) =
-                pack2<F16>(__builtin_fmaf(a, sv, mv), __builtin_fmaf(b, sv, mv));
-        }
+        for (int i = 0; i < NW; ++i)
+            st16(vo + 64 * i, *turn.chunk(i));
+        Turn<D>::done();
     }
 }
 

@@ -174,17 +174,18 @@ struct AttnI4 {
     int32_t causal, window;
     float scale;
 };
-// How a call is cut: `cols` rows (of one key-value head: tokens times the heads that share it)
-// to a tile, and the tokens of a sequence over `splits` workgroups, whose partial results the
-// workspace holds.
+// How a call is cut.  The rows of one cache head (tokens times the heads that share it) go into
+// tiles; few rows: all sequences' tokens are dealt out to `dealt` workgroups, many rows: the tokens of
+// a sequence to `splits` of them.  The workspace holds their partial results.
 struct AttnPlan {
     bool by_rows;      // waves of a workgroup take rows of their own, not tokens
     int cols;          // blocks of 16 rows to a wave
-    int tiles, splits;
+    int tiles, splits, dealt;
     int64_t ws_bytes;
 };
+// Of the groups, 64 takes the largest workspace.
 AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
-                   int kv_heads, int dim);
+                   int kv_heads, int dim, int group);
 hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStream_t stream);
 
 }  // namespace bq

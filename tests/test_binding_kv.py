@@ -29,7 +29,7 @@ def lib(monkeypatch):
     recorder = Recorder()
     bq._L()
     monkeypatch.setattr(bq, "_lib", recorder)
-    monkeypatch.setattr(bq, "_raw_device", None)
+    monkeypatch.setattr(bq, "_raw_device", lambda: -1)      # tensors on the host stand for the GPU's
     return recorder
 
 
@@ -112,8 +112,7 @@ def test_rows(lib, name):
         call(rows(), rows(), slots, c, "_f16")
     for bad in ((rows(4), rows(), slots, c), (rows(), rows(6), slots, c), (rows(), rows()[:, :1], slots, c),
                 (rows(), torch.zeros((5, H, 2 * D), dtype=BF)[..., ::2], slots, c),
-                (rows(), rows(), torch.zeros(10, dtype=I32)[::2], c),
-                (rows().to("meta"), rows(), slots, c), (rows(), rows(), slots.to("meta"), c)):
+                (rows(), rows(), torch.zeros(10, dtype=I32)[::2], c)):
         with pytest.raises(ValueError):
             call(*bad)
     assert not lib.calls
@@ -156,19 +155,38 @@ def test_attention_refusals(lib):
                 dict(out=z((7, 2, D), dtype=BF)), dict(q=z((7, 4, 2 * D), dtype=BF)[..., ::2]),
                 dict(table=z((3, 10), dtype=I32)[:, ::2]), dict(lens=z(2, dtype=I32)), dict(lens=z(4, dtype=I32)),
                 dict(lens=z(6, dtype=I32)[::2]), dict(starts=z(3, dtype=I32)), dict(starts=z(5, dtype=I32)),
-                dict(lse=z(27)), dict(lse=z((4, 7)).t()), dict(max_q=None), dict(ws=z(10, 10).t()),
-                dict(q=z((7, 4, D), dtype=BF, device="meta")), dict(lens=z(3, dtype=I32, device="meta")),
-                dict(lse=z((7, 4), device="meta")), dict(ws=z(100, device="meta")),
-                dict(starts=z(4, dtype=I32, device="meta"))):
+                dict(lse=z(27)), dict(lse=z((4, 7)).t()), dict(max_q=None), dict(ws=z(10, 10).t())):
         with pytest.raises(ValueError):
             bq.bq_attn_i4(**attn_args(**bad))
     assert not lib.calls
 
 
+class There:
+    """A tensor that says it is on another device."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return (lambda: 1) if name == "get_device" else getattr(self.t, name)
+
+
+def test_tensors_on_another_device_than_the_cache(lib):
+    slots, c = torch.zeros(5, dtype=I32), cache()
+    for bad in ((There(rows()), rows(), slots), (rows(), There(rows()), slots), (rows(), rows(), There(slots))):
+        with pytest.raises(ValueError):
+            bq.bq_kv_write_i4(*bad, c, stream=0)
+        with pytest.raises(ValueError):
+            bq.bq_kv_read_i4(c, bad[2], bad[0], bad[1], stream=0)
+    good = attn_args()
+    for name in ("q", "table", "lens", "out", "starts", "lse", "ws"):
+        with pytest.raises(ValueError):
+            bq.bq_attn_i4(**attn_args(**{name: There(good[name])}))
+    assert not lib.calls
+
+
 def test_another_device_than_the_current_one(lib, monkeypatch):
     """The launch would go to the current device's stream."""
-    class There:
-        index = 1
     c = cache()
     monkeypatch.setattr(bq, "_raw_device", lambda: 0)
     for call in (lambda: bq.bq_kv_write_i4(rows(), rows(), torch.zeros(5, dtype=I32), c, stream=0),
