@@ -89,6 +89,11 @@ __device__ __forceinline__ float bcast(float v) {
                                                               0xF, true));
 }
 
+template <int Lane>
+__device__ __forceinline__ uint32_t bcast_u(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + Lane, 0xF, 0xF, true);
+}
+
 template <bool F16>
 __device__ __forceinline__ float lo16(uint32_t w) {
     if constexpr (F16)
@@ -1035,10 +1040,10 @@ struct Rows : State<D, G, F16, NC> {
     int wg_lo, wg_hi;
     float k2;                   // the k above
 
-    // What a lane has loaded of a turn.  Of values: codes, scales of its groups' 8 tokens, scales of
-    // one or a few of all groups; of keys: codes, an entry's scales of key and value.
+    // What a lane has loaded of a turn.  Of values: codes, a token's scales in each of its wave's
+    // groups, one or a few of all groups'; of keys: codes, an entry's scales of key and value.
     struct Raw {
-        uint32_t w[4], s[8 * GV], t[NB];
+        uint32_t w[4], s[2], t[NB];
         bool ok;
     };
 
@@ -1109,7 +1114,7 @@ struct Rows : State<D, G, F16, NC> {
             const int group = part_of * VB * 16 / G;
 #pragma unroll
             for (int k = 0; k < GV; ++k)
-                ld_words<8>(s + 4 * (int64_t)(group + k) * c.page_size, x.s + 8 * k);
+                x.s[k] = *reinterpret_cast<const uint32_t*>(s + 4 * ((int64_t)(group + k) * c.page_size + (r & 7)));
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int e = NG == 1 ? r & 7 : 16 * i + r;
@@ -1157,45 +1162,39 @@ struct Rows : State<D, G, F16, NC> {
         }
         // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 are within
         uint32_t top = 0;
-        bool any_wild = false;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; !F16 && i < NB; ++i) {
             const float s = lo16<F16>(x.t[i]), m = hi16<F16>(x.t[i]);
             const float v = __builtin_fabsf(__builtin_fmaf(8.0f, s, m)) + 8.0f * __builtin_fabsf(s);
             const int t = tok + step_of * kStep + 8 * g + (r & 7);
-            const bool bad = wild(x.t[i]), out = !x.ok || t < wg_lo || t >= wg_hi;
-            any_wild = any_wild || bad || out;
-            top = max(top, bad || out ? 0u : __float_as_uint(v));
+            const bool out = wild(x.t[i]) || !x.ok || t < wg_lo || t >= wg_hi;
+            top = max(top, out ? 0u : __float_as_uint(v));
         }
         int b = 0;
         if constexpr (!F16) {
             top = row_max16(top);
             b = clampi(15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top)), -112, 100);
         }
-        any_wild = __any(any_wild);
+        // a lane scales one token's pair for each of its groups, and the quarter wave shares them
         h16x2 s2[GV][4], m2[GV][4];
-#pragma unroll
-        for (int k = 0; k < GV; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float s[2], m[2];
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    uint32_t w = x.s[8 * k + 2 * i + o];
-                    if (any_wild) {
-                        const int t = tok + step_of * kStep + 8 * g + 2 * i + o;
-                        w = wild(w) || !x.ok || t < wg_lo || t >= wg_hi ? 0u : w;
-                    }
-                    s[o] = lo16<F16>(w);
-                    m[o] = __builtin_fmaf(8.0f, s[o], hi16<F16>(w));
-                    if constexpr (!F16) {
-                        s[o] = __builtin_ldexpf(s[o], b);
-                        m[o] = __builtin_ldexpf(m[o], b);
-                    }
-                }
-                s2[k][i] = __builtin_convertvector(f32x2{s[0], s[1]}, h16x2);
-                m2[k][i] = __builtin_convertvector(f32x2{m[0], m[1]}, h16x2);
+        const int tok_of = tok + step_of * kStep + 8 * g + (r & 7);
+        const bool seen = x.ok && tok_of >= wg_lo && tok_of < wg_hi;
+        S::template unroll<GV>([&](auto gi) {
+            constexpr int k = decltype(gi)::value;
+            const uint32_t w = wild(x.s[k]) || !seen ? 0u : x.s[k];
+            float s = lo16<F16>(w), m = __builtin_fmaf(8.0f, s, hi16<F16>(w));
+            if constexpr (!F16) {
+                s = __builtin_ldexpf(s, b);
+                m = __builtin_ldexpf(m, b);
             }
+            const uint32_t pair = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{s, m}, h16x2));
+            S::template unroll<4>([&](auto ti) {
+                constexpr int i = decltype(ti)::value;
+                const uint32_t even = bcast_u<2 * i>(pair), odd = bcast_u<2 * i + 1>(pair);
+                s2[k][i] = __builtin_bit_cast(h16x2, __builtin_amdgcn_perm(odd, even, 0x05040100u));
+                m2[k][i] = __builtin_bit_cast(h16x2, __builtin_amdgcn_perm(odd, even, 0x07060302u));
+            });
+        });
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
             const int j = part_of * VB + i;
@@ -1215,12 +1214,13 @@ struct Rows : State<D, G, F16, NC> {
                 f32x2{(float)b, x.ok ? 1.0f : 0.0f};
     }
 
-    // 32 tokens: step `sub` of a turn's operands.
+    // 32 tokens: step `sub` of a turn's operands.  One body, masked or not: with two of them the
+    // results are copied where they meet.
     __device__ __forceinline__ void step(const char* buf, int sub, int tok) {
-        const Src src{buf, lane, g, sub};
         const f32x2 bo = *reinterpret_cast<const f32x2*>(buf + kB + 8 * (sub * 4 + g));
         const float b = bo.x;
         const bool ok = bo.y != 0.0f;
+        const Src src{buf, lane, g, sub};
         float x[NC][8];
         this->scores(src, x);
         if (!(tok >= this->full_lo && tok + kStep <= this->full_hi && __all(ok))) {
