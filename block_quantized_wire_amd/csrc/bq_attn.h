@@ -66,8 +66,11 @@ struct Div {
 
 struct Args {
     AttnI4 a;
-    Div units;          // seqs * cache heads * splits
     Div heads, by_splits;
+    Div cells;          // cache heads * splits
+    Div inner;          // by_seq: tiles, else seqs
+    int32_t by_seq;     // workgroups go by sequence, then tile; else by tile, then sequence
+    int32_t groups;     // workgroups: seqs * tiles * cells
     Div share;          // heads of q to one of the cache
     Div bpp;            // blocks of 8 tokens to a page
     int32_t tiles, splits;
@@ -434,16 +437,60 @@ struct Walk {
     }
 };
 
-// A workgroup's place among the sequences, heads, splits and tiles; the last tiles, which see the
-// most under a causal mask, start first.
+// The s-th sequence of a batch, long ones first: by eighths of the longest's length, within one as
+// they come.  Workgroups are started in their order, and a long one that starts last is waited for.
+__device__ __forceinline__ int by_length(const AttnI4& a, int s) {
+    constexpr int N = kMaxDealt / 64;
+    if (a.seqs == 1 || a.seqs > kMaxDealt)
+        return s;
+    const int lane = threadIdx.x & 63;
+    int len[N], most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int b = 64 * i + lane;
+        len[i] = b < a.seqs ? clampi(a.lens[b], 0, a.max_len) : -1;
+        most = len[i] > most ? len[i] : most;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int m = __shfl_xor(most, d);
+        most = m > most ? m : most;
+    }
+    most = __builtin_amdgcn_readfirstlane(most);
+    int part = 7;
+    while (true) {
+        // lengths of (part, part + 1] eighths; the last part takes 0 too
+        const int from = (int)((int64_t)most * part >> 3), to = (int)((int64_t)most * (part + 1) >> 3);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool in = len[i] >= 0 && len[i] <= to && (len[i] > from || part == 0);
+            const uint64_t m = __ballot(in);
+            const int n = __popcll(m);
+            if (s < n) {
+                const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                                             __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+                return 64 * i + __ffsll((unsigned long long)__ballot(in && before == s)) - 1;
+            }
+            s -= n;
+        }
+        if (--part < 0)
+            return 0;       // every sequence is in one part
+    }
+}
+
+// A workgroup's place among the sequences, heads, splits and tiles.  Heads are next to each other;
+// the last tiles, which see the most under a causal mask, start first, or where all tiles of a
+// sequence see about as much, the long sequences.
 struct Place {
     int tile, head, split, seq;
     __device__ __forceinline__ explicit Place(const Args& p) {
-        tile = p.tiles - 1 - p.units.div(blockIdx.x);
-        const int unit = p.units.mod(blockIdx.x), rest = p.heads.div(unit);
-        head = p.heads.mod(unit);
-        split = p.by_splits.mod(rest);
-        seq = p.by_splits.div(rest);
+        const int n = (int)blockIdx.x;
+        const int cell = p.cells.div(n), rest = n - cell * (int)p.cells.d;      // heads, splits
+        const int outer = p.inner.div(cell), in = cell - outer * (int)p.inner.d;
+        tile = p.tiles - 1 - (p.by_seq ? in : outer);
+        seq = by_length(p.a, p.by_seq ? outer : in);
+        split = p.heads.div(rest);
+        head = rest - split * p.a.c.heads;
     }
 };
 
@@ -1468,7 +1515,7 @@ hipError_t launch_width(std::integral_constant<int, 256>, const Args& a, const A
 
 template <int D, int G, bool F16>
 hipError_t launch_group(const Args& a, const AttnPlan& p, hipStream_t st) {
-    const dim3 grid(a.units.d * (unsigned)a.tiles), block(kThreads);
+    const dim3 grid((unsigned)a.groups), block(kThreads);
     hipError_t e;
     if (a.dealt)
         e = launch1(k_attn_tokens<D, G, F16, true>, dim3((unsigned)a.dealt), block, st, a);

@@ -51,9 +51,13 @@ hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStrea
     attn::Args g{};
     g.a = a;
     using attn::Div;
-    g.units = Div::by((uint32_t)((int64_t)a.seqs * a.c.heads * p.splits));
     g.heads = Div::by(a.c.heads);
     g.by_splits = Div::by(p.splits);
+    g.cells = Div::by(a.c.heads * p.splits);
+    // new rows that are half of a sequence or less see most of it, each
+    g.by_seq = !a.causal || 2 * (int64_t)a.max_q <= a.max_len;
+    g.inner = Div::by(g.by_seq ? p.tiles : a.seqs);
+    g.groups = (int32_t)((int64_t)a.seqs * p.tiles * a.c.heads * p.splits);
     g.share = Div::by(a.heads / a.c.heads);
     g.bpp = Div::by(a.c.page_size / 8);
     g.tiles = p.tiles;
