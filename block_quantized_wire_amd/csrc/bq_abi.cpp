@@ -9,6 +9,7 @@
 #include "blockq_kv.h"
 #include "blockq_moe.h"
 
+#include <cmath>
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -1473,7 +1474,7 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
     BQ_TRY(check_kv(cache));
     const bq_kv_i4& c = *cache;
     BQ_TRY(check_attn_sizes(seqs, rows, max_q, max_len, heads, c.heads));
-    if (table_cols < 0 || table_cols > kMaxLen || window < 0)
+    if (table_cols < 0 || table_cols > kMaxLen || window < 0 || !std::isfinite(scale))
         return BQ_ERR_SIZE;
     if (seqs == 0 || rows == 0 || max_q == 0)
         return BQ_OK;
@@ -1493,7 +1494,8 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
         return BQ_ERR_SCRATCH;
     if (plan.ws_bytes > 0 && !aligned(ws, 16))
         return BQ_ERR_ALIGN;
-    if (seqs * c.heads * plan.tiles * plan.splits >= (int64_t)1 << 24 ||
+    // a launch holds less than 2^32 threads
+    if (seqs * c.heads * plan.tiles * plan.splits >= (int64_t)1 << (plan.by_rows ? 23 : 24) ||
         (plan.ws_bytes > 0 && seqs * (starts ? max_q : 1) * heads >= (int64_t)1 << 24))
         return BQ_ERR_SIZE;
     ins[4] = rows_span(q, rows, ldq, heads, hsq, c.dim);

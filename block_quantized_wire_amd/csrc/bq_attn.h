@@ -48,13 +48,13 @@ constexpr int kMaxSplits = 256;     // of the tokens of a sequence
 constexpr int kMaxDealt = 256;      // sequences whose turns are dealt out
 constexpr float kRaise = 8.0f;      // a score may pass R by this, in powers of two
 
-// Division of n < 2^27 by a d known to the host: with 2^(p - 27) >= d and mul = ceil(2^p / d),
-// n * mul passes n * 2^p / d by less than 2^p / d, which no quotient notices.
+// Division of n < 2^28 by a d <= 2^28 known to the host: with 2^(p - 28) >= d and mul =
+// ceil(2^p / d), n * mul passes n * 2^p / d by less than 2^p / d, which no quotient notices.
 struct Div {
     uint32_t d, mul, p;
     static Div by(uint32_t d) {
-        uint32_t p = 27;
-        while (((uint64_t)1 << (p - 27)) < d)
+        uint32_t p = 28;
+        while (((uint64_t)1 << (p - 28)) < d)
             ++p;
         return Div{d, (uint32_t)((((uint64_t)1 << p) + d - 1) / d), p};
     }
@@ -80,7 +80,9 @@ struct Args {
     // the turns are dealt out [workgroup][2][16][D]
     float* part;
     float* ml;
-    int32_t* found;     // where turns are dealt out: [kMaxDealt][2] turns, turns up to there; all of them
+    // where turns are dealt out: [kMaxDealt][2] a sequence's turns in one unit, all of a cache head
+    // up to its end; then those of all sequences
+    int32_t* found;
 };
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
@@ -512,6 +514,10 @@ __device__ __forceinline__ int turns_of(const AttnI4& a, int b) {
     const int lo = a.window > 0 && first > 0 ? first : 0;
     const int blocks = (s.len + 7) / 8 - lo / 32 * 4;
     return s.n > 0 && blocks > 0 ? (blocks + kTurn - 1) / kTurn : 0;
+}
+// Tiles of 16 rows of sequence b.
+__device__ __forceinline__ int tiles_of(const AttnI4& a, int b, const Div& share) {
+    return (seq_of(a, b).n * (int)share.d + 15) / 16;
 }
 
 // `total` turns dealt out to `groups` workgroups, each one a run of them.
@@ -977,7 +983,6 @@ struct Tokens : State<D, G, F16, 1> {
         }
         // every wave adds up the sequences' turns: lane i finds those of i, i + 64, ..; one of them
         // leaves in LDS how many each has, and all up to its end
-        const int units = a.c.heads * p.tiles;
         int past[kMaxDealt / 64], sum = 0;
 #pragma unroll
         for (int i = 0; i < kMaxDealt / 64; ++i) {
@@ -985,7 +990,7 @@ struct Tokens : State<D, G, F16, 1> {
             past[i] = 0;
             if (64 * i < a.seqs) {
                 const int n = b < a.seqs ? turns_of(a, b) : 0;
-                int v = n;
+                int v = b < a.seqs ? n * tiles_of(a, b, p.share) : 0;
 #pragma unroll
                 for (int d = 1; d < 64; d <<= 1) {
                     const int u = __shfl_up(v, d);
@@ -1003,7 +1008,8 @@ struct Tokens : State<D, G, F16, 1> {
         }
         if (blockIdx.x == 0 && threadIdx.x == 0)
             p.found[2 * kMaxDealt] = sum;
-        const Deal deal(sum * units, p.dealt);
+        const int heads = a.c.heads;
+        const Deal deal(sum * heads, p.dealt);
         const int w = (int)blockIdx.x;
         int at = deal.first(w);
         const int end = deal.first(w + 1);
@@ -1013,16 +1019,17 @@ struct Tokens : State<D, G, F16, 1> {
 #pragma unroll
         for (int i = 0; i < kMaxDealt / 64; ++i)
             if (64 * i < a.seqs)
-                b += __popcll(__ballot(64 * i + lane < a.seqs && past[i] * units <= at));
+                b += __popcll(__ballot(64 * i + lane < a.seqs && past[i] * heads <= at));
         __syncthreads();
         int count = __builtin_amdgcn_readfirstlane(turns[b]);
-        const int before = __builtin_amdgcn_readfirstlane(turns[kMaxDealt + b]) - count;
-        int unit = (int)((uint32_t)(at - before * units) / (uint32_t)count);
-        int t = at - before * units - unit * count;
+        int units = tiles_of(a, b, p.share) * heads;
+        const int before = __builtin_amdgcn_readfirstlane(turns[kMaxDealt + b]) * heads - count * units;
+        int unit = (int)((uint32_t)(at - before) / (uint32_t)count);
+        int t = at - before - unit * count;
         while (true) {
             const int take = end - at < count - t ? end - at : count - t;
             const int tile = p.heads.div(unit);
-            segment(lds, b, unit - tile * a.c.heads, tile, t, take,
+            segment(lds, b, unit - tile * heads, tile, t, take,
                     take == count ? -1 : 2 * w + (t == 0 ? 1 : 0));
             at += take;
             if (at >= end)
@@ -1033,6 +1040,7 @@ struct Tokens : State<D, G, F16, 1> {
                 do
                     count = __builtin_amdgcn_readfirstlane(turns[++b]);
                 while (count == 0);
+                units = tiles_of(a, b, p.share) * heads;
             }
         }
     }
@@ -1441,10 +1449,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(Args p) {
     int count = p.splits;
     int64_t from = cell, next = cell + cells, step = cells;
     if (p.dealt) {
-        const int units = a.c.heads * p.tiles, mine = p.found[2 * b];
+        const int heads = a.c.heads, mine = p.found[2 * b], tiles = tiles_of(a, b, p.share);
         const int share = (int)p.share.d, r = qi * share + p.share.mod(hd);     // row of its cache head
-        const int first = (p.found[2 * b + 1] - mine) * units + (r / 16 * a.c.heads + p.share.div(hd)) * mine;
-        const Deal deal(p.found[2 * kMaxDealt] * units, p.dealt);
+        const int first =
+            (p.found[2 * b + 1] - mine * tiles) * heads + (r / 16 * heads + p.share.div(hd)) * mine;
+        const Deal deal(p.found[2 * kMaxDealt] * heads, p.dealt);
         count = 0;
         if (mine > 0) {
             const int w0 = deal.of(first), w1 = deal.of(first + mine - 1);

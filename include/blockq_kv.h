@@ -79,7 +79,8 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  *   out_d = bf16_rne( sum over t of exp(score_t - lse) * v_td ).
  * A row at place p sees tokens [0, lens[b]); with causal != 0 those up to p; with window > 0
  * those after p - window.  A row that sees nothing becomes 0, its lse -inf.  Rows of no
- * sequence are not written.  Tokens that a row does not see have no effect on it, whatever their
+ * sequence are not written.  scale is finite (else BQ_ERR_SIZE); where |scale| times a number of
+ * q passes 2^117, that row and head may become NaN.  Tokens that a row does not see have no effect on it, whatever their
  * codes and scales hold (but for the bits that much larger scales of v cost, see below).
  *
  * Scores, softmax and sums are in binary32; q is exact but for numbers 2^-24 below the largest of
@@ -92,12 +93,16 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  *
  * q, out: row stride ldq, ldo, head stride hsq, hso entries, multiples of 8, 16-byte aligned;
  * rows and heads of out must not overlap.  table: int32, `table_cols` <= ldt entries a sequence;
- * lens: int32[seqs]; starts: int32[seqs + 1], ascending, or NULL.  lse: float[rows][heads] or NULL.
+ * lens: int32[seqs]; starts: int32[seqs + 1], ascending, or NULL
+ * (max_q is then taken as 1).  lse: float[rows][heads] or NULL.
  * max_q, max_len: at least every n_b and lens[b]; 0 <= lens[b].  What the arrays hold beyond
  * that is brought inside: lens to [0, min(max_len, table_cols * page_size)], rows of a sequence
  * beyond max_q are not computed, and the tokens of a page outside [0, pages) are seen by no row.
  * heads is a multiple of cache->heads, at most 64 times as many; seqs, max_q <= 2^20, rows *
- * heads < 2^31, max_len < 2^30 (else BQ_ERR_SIZE).
+ * heads < 2^31, max_len < 2^30 (else BQ_ERR_SIZE).  With n = max_q * heads / cache->heads rows to a
+ * sequence and head of the cache, seqs * cache->heads * ceil(n / 16) is below 2^24 for n <= 64, and
+ * seqs * cache->heads * ceil(n / 128) below 2^23 else; where ws is used, so are seqs * max_q * heads
+ * 2^24 (else BQ_ERR_SIZE).
  * ws: scratch of at least bq_attn_i4_ws_bytes bytes, 16-byte aligned, never more than 64 MiB,
  * NULL where that is 0; its contents do not matter, and calls that may run at the same time
  * (two streams, two graphs) need one each. */

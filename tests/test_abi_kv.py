@@ -153,7 +153,8 @@ def test_attention_refusals(suffix):
     for bad in (dict(seqs=-1), dict(seqs=(1 << 20) + 1), dict(rows=-1), dict(rows=1 << 29), dict(max_q=-1),
                 dict(max_q=(1 << 20) + 1), dict(max_len=-1), dict(max_len=1 << 30), dict(heads=0),
                 dict(heads=-2), dict(heads=3), dict(heads=130), dict(table_cols=-1), dict(window=-1),
-                dict(seqs=1 << 20, max_q=1 << 20)):
+                dict(seqs=1 << 20, max_q=1 << 20), dict(seqs=1 << 20, max_q=512, rows=7),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-float("inf"))):
         refuse(call, SIZE, **bad)
     for bad in ("q", "table", "lens", "out"):
         refuse(call, NULL, **{bad: None})

@@ -139,7 +139,9 @@ def test_shared_heads(share):
 
 
 @pytest.mark.parametrize("lens,new,heads,kv_heads", [((20000,), None, 8, 1), ((9001, 3), (2, 1), 8, 1),
-                                                     ((5003,), (40,), 4, 2), ((4100, 4000), (130, 3), 2, 1)])
+                                                     ((5003,), (40,), 4, 2), ((4100, 4000), (130, 3), 2, 1),
+                                                     ((5000, 3000, 10, 0, 700), (1, 8, 5, 0, 2), 8, 1),
+                                                     ((0, 900, 4000, 0), (3, 0, 1, 16), 8, 2)])
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 def test_split_over_the_tokens(lens, new, heads, kv_heads, kind):
     """Few rows and many tokens: workgroups share a sequence and their results are joined."""
