@@ -375,6 +375,15 @@ struct State {
                 __builtin_amdgcn_sched_barrier(0);
         });
     }
+    // Scores are numbers from here on: else the compiler takes their last steps behind the branch
+    // that follows, with the operands of all of them, and spills.
+    static __device__ __forceinline__ void settle(float (&x)[NC][8]) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                asm("" : "+v"(x[c][i]));
+    }
     // Whether row c sees token t of a page that is there.
     __device__ __forceinline__ bool sees(int c, int t) const {
         return t >= seen_lo[c] && t < seen_hi[c] && t < hi;
@@ -1278,6 +1287,7 @@ struct Rows : State<D, G, F16, NC> {
         const Src src{buf, lane, g, sub};
         float x[NC][8];
         this->scores(src, x);
+        S::settle(x);
         if (!(tok >= this->full_lo && tok + kStep <= this->full_hi && __all(ok))) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
