@@ -1584,7 +1584,10 @@ int64_t bq_attn_i4_ws_bytes(int64_t seqs, int64_t rows, int64_t max_q, int64_t m
         return -1;
     if (seqs == 0 || rows == 0 || max_q == 0)
         return 0;
-    return bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim, 64).ws_bytes;
+    // for a cache in groups of any size: small ones are dealt out sooner, wide ones to more workgroups
+    const int64_t small = bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim, 32).ws_bytes;
+    const int64_t wide = bq::attn_plan(seqs, rows, max_q, max_len, heads, kv_heads, dim, 64).ws_bytes;
+    return small > wide ? small : wide;
 }
 
 // ---- E4M3 128-block codec ------------------------------------------------------------------

@@ -101,8 +101,8 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  * heads is a multiple of cache->heads, at most 64 times as many; seqs, max_q <= 2^20, rows *
  * heads < 2^31, max_len < 2^30 (else BQ_ERR_SIZE).  With n = max_q * heads / cache->heads rows to a
  * sequence and head of the cache, seqs * cache->heads * ceil(n / 16) is below 2^24 for n <= 64, and
- * seqs * cache->heads * ceil(n / 128) below 2^23 else; where ws is used, so are seqs * max_q * heads
- * 2^24 (else BQ_ERR_SIZE).
+ * seqs * cache->heads * ceil(n / 128) below 2^23 else; where ws is used, seqs * max_q * heads
+ * is below 2^24 (else BQ_ERR_SIZE).
  * ws: scratch of at least bq_attn_i4_ws_bytes bytes, 16-byte aligned, never more than 64 MiB,
  * NULL where that is 0; its contents do not matter, and calls that may run at the same time
  * (two streams, two graphs) need one each. */

@@ -156,6 +156,19 @@ def test_split_over_the_tokens(lens, new, heads, kv_heads, kind):
     c.check(window=700)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("new,window", [(None, 0), ((3, 0, 9, 1, 2), 0), ((2, 5, 16, 0, 1), 1000)])
+def test_turns_dealt_out(dim, group, kind, new, window):
+    """Few rows of a ragged batch with one long sequence: its turns go to many workgroups, those of short
+    ones to some of them as well."""
+    say(f"attn dealt D={dim} G={group} {kind} new={new} window={window}")
+    lens = (2805, 0, 33, 1400, 7)
+    c = Case([dim, group], lens, new, 8, 2, dim, group, 24, kind)
+    assert bq.bq_attn_i4_ws_bytes(len(lens), c.q.shape[0], c.max_q, max(lens), 8, 2, dim) > 0
+    c.check(window=window)
+
+
 def test_rows_behind_the_last_sequence_are_left():
     for new, extra in ((None, 5), ((3, 8), 7), ((80, 2), 1)):
         c = Case([extra], (50, 90), new, 4, 2, 128, 32, 8, "bf16")
