@@ -1340,7 +1340,8 @@ int64_t kv_scale_bytes(const bq_kv_i4& c) { return (int64_t)c.page_size * (c.dim
 bq_status check_kv_arrays(const bq_kv_i4& c, Span s[4]) {
     if (!c.k || !c.v || !c.ks || !c.vs)
         return BQ_ERR_NULL;
-    if (c.spage_stride > kMaxExtentBytes || c.shead_stride > kMaxExtentBytes)
+    if (c.spage_stride < 0 || c.shead_stride < 0 || c.spage_stride > kMaxExtentBytes ||
+        c.shead_stride > kMaxExtentBytes)
         return BQ_ERR_BOUNDS;
     const int64_t codes = kv_code_bytes(c), scales = kv_scale_bytes(c);
     if (!nest_fits(c.pages, c.page_stride, c.heads, c.head_stride, codes, true) ||
@@ -1478,7 +1479,7 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
         return BQ_ERR_SIZE;
     if (seqs == 0 || rows == 0 || max_q == 0)
         return BQ_OK;
-    if (!table || !lens)
+    if ((!table && table_cols > 0) || !lens)
         return BQ_ERR_NULL;
     Span ins[8];
     BQ_TRY(check_kv_arrays(c, ins));

@@ -109,6 +109,7 @@ def test_pools_that_are_refused(suffix):
         for bad in (dict(head_stride=1023), dict(head_stride=512), dict(page_stride=1024), dict(page_stride=0),
                     dict(head_stride=-1024), dict(page_stride=1 << 50), dict(spage_stride=64),
                     dict(shead_stride=32), dict(shead_stride=0), dict(spage_stride=-128),
+                    dict(spage_stride=-(1 << 63)), dict(shead_stride=-(1 << 63)),
                     dict(spage_stride=1 << 62), dict(shead_stride=1 << 48), dict(page_stride=1 << 62)):
             refuse(call, BOUNDS, **{"cache_" + k: v for k, v in bad.items()})
         for bad in (dict(page_stride=2056), dict(head_stride=1032, page_stride=4096), dict(spage_stride=132),

@@ -131,6 +131,17 @@ def test_rows_that_see_nothing():
             c.check(causal=False, window=3)
 
 
+@pytest.mark.parametrize("new", [None, (3, 1), (70, 2)])
+def test_tables_without_a_page(new):
+    """Rows of sequences that have no page: nothing is read of a table that has no column."""
+    say(f"attn no pages new={new}")
+    c = Case([1], (0, 0), new, 4, 2, 64, 32, 16, "bf16")
+    c.table = c.table[:, :0]
+    out, lse = c.run(max_len=0)
+    sync()
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
 @pytest.mark.parametrize("share", [1, 2, 3, 5, 7, 8, 16, 17, 32, 64])
 def test_shared_heads(share):
     for new in (None, (3, 1), (9, 2)):
