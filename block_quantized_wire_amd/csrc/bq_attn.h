@@ -159,12 +159,12 @@ __device__ __forceinline__ h16x8 codes8(uint32_t w) {
         h16x8, u32x4{w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u});
 }
 
-// Codes c of the low bits of both half-words as c - 8: 1024 + c is a binary16 number with c in its
+// Codes of the low bits of both half-words as numbers: 1024 + c is a binary16 number with c in its
 // low bits.  v_and_or_b32 takes one constant that is not in a vector register.
-__device__ __forceinline__ uint32_t centred(uint32_t w) {
+__device__ __forceinline__ uint32_t numbers(uint32_t w) {
     uint32_t one = 0x64006400u;
     asm("" : "+v"(one));
-    const h16x2 off{(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const h16x2 off{(_Float16)-1024.0f, (_Float16)-1024.0f};
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, (w & 0x000F000Fu) | one) + off);
 }
 
@@ -1076,8 +1076,8 @@ __global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void
 // operand is 64 lanes * 16 bytes in the lanes' order, so neither side meets a bank conflict.  Four
 // waves unpack values, the other four keys and their scales.
 //
-// Values become binary16 numbers here, (c - 8) s + (m + 8 s) in one rounding, so that p needs no
-// scale of each group.  For that the 8 tokens of a block take a power of two 2^b that brings their
+// Values become binary16 numbers here, c s + m in one rounding, so that p needs no scale of each
+// group.  For that the 8 tokens of a block take a power of two 2^b that brings their
 // largest to just below 2^15 (1 in the _f16 kernels, whose values fit); a quarter wave's 8 tokens of
 // p are one block, so p takes 2^(k - b) there, k the least b so far.
 //
@@ -1234,7 +1234,7 @@ struct Rows : State<D, G, F16, NC> {
             }
             return;
         }
-        // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 are within
+        // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 and m are within
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; !F16 && i < NB; ++i) {
@@ -1256,12 +1256,11 @@ struct Rows : State<D, G, F16, NC> {
         S::template unroll<GV>([&](auto gi) {
             constexpr int k = decltype(gi)::value;
             const uint32_t w = wild(x.s[k]) || !seen ? 0u : x.s[k];
-            float s = lo16<F16>(w), m = __builtin_fmaf(8.0f, s, hi16<F16>(w));
+            uint32_t pair = w;
             if constexpr (!F16) {
-                s = __builtin_ldexpf(s, b);
-                m = __builtin_ldexpf(m, b);
+                const f32x2 two{__builtin_ldexpf(lo16<F16>(w), b), __builtin_ldexpf(hi16<F16>(w), b)};
+                pair = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, h16x2));
             }
-            const uint32_t pair = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{s, m}, h16x2));
             S::template unroll<4>([&](auto ti) {
                 constexpr int i = decltype(ti)::value;
                 const uint32_t even = bcast_u<2 * i>(pair), odd = bcast_u<2 * i + 1>(pair);
@@ -1277,7 +1276,7 @@ struct Rows : State<D, G, F16, NC> {
             for (int tp = 0; tp < 4; ++tp) {
                 // D == 64: blocks 2 part and 2 part + 1 of the same words
                 const uint32_t w = x.w[tp] >> (D == 64 ? 8 * part_of + 4 * i : 4 * i);
-                const h16x2 c = __builtin_bit_cast(h16x2, centred(w));
+                const h16x2 c = __builtin_bit_cast(h16x2, numbers(w));
                 op[tp] = __builtin_bit_cast(
                     uint32_t, __builtin_elementwise_fma(c, s2[16 * i / G][tp], m2[16 * i / G][tp]));
             }

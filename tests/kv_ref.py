@@ -10,7 +10,9 @@ import torch
 
 TORCH = {"bf16": torch.bfloat16, "f16": torch.float16}
 HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}      # what one rounding may cost, relative
-HELD = {"bf16": 2.0 ** -12, "f16": 2.0 ** -20}     # a weight times a scale, relative
+# a weight times a scale, relative: binary16 has 11 significant bits, so a number in [2^e, 2^(e+1)) lies
+# within half of 2^(e-10) of its rounding, 2^-11 of 2^e or less; two such parts hold it to 2^-22
+HELD = {"bf16": 2.0 ** -11, "f16": 2.0 ** -20}
 TINY = {"bf16": 0.0, "f16": 2.0 ** -25}            # ... and absolute
 
 
@@ -119,11 +121,10 @@ def attend(pool, q, table, lens, starts, causal, window, scale, kind):
     most dim terms in any order and 2^-23 a step (which covers any rounding of the matrix
     cores), over the sum of the terms' sizes; q's own rounding (2^-25 of the largest of its row, 2^4
     times that for half of its numbers) is below a step.  A weight is off by that and by exp2's and
-    the reference's rounding; weights times scales are held to 2^-20 (for bf16
-    results to 11 bits: half a step is 2^-12); where there are many rows a value is a binary16 number
-    (c - 8) s + (m + 8 s), its second term another: half a step, 2^-12, of either; sums over the
-    tokens take a step for 8 tokens and a few more to join, over the sizes of (c - 8) s and of
-    m + 8 s."""
+    the reference's rounding; weights times scales are held to 2^-20 (for bf16 results to 11 bits:
+    half a step is 2^-11 at most); where there are many rows a value is a binary16 number, c s + m
+    rounded once: 2^-11 of it at most; sums over the tokens take a step for 8 tokens and a few more
+    to join, over the sizes of (c - 8) s and of m + 8 s."""
     rows, heads, dim = q.shape
     share = heads // pool.heads
     out, lse = np.zeros((rows, heads, dim)), np.full((rows, heads), -np.inf)
@@ -169,8 +170,7 @@ def attend(pool, q, table, lens, starts, causal, window, scale, kind):
                 parts = np.abs(vc[on, c] - 8) * np.abs(vs[on, c]) + np.abs(vm[on, c] + 8 * vs[on, c])
                 sums = ulp * (n / 8 + 32)
                 e = ((w * (off + mean + HELD[kind] + sums))[:, None] * parts).sum(0)
-                middle = np.abs(vm[on, c] + 8 * vs[on, c])
-                e += (w[:, None] * (np.abs(v) + middle)).sum(0) * 2.0 ** -12
+                e += (w[:, None] * np.abs(v)).sum(0) * 2.0 ** -11
                 # m + 8 s is rounded for each token
                 e += ((w * ulp)[:, None] * (np.abs(vm[on, c]) + 8 * np.abs(vs[on, c]))).sum(0)
                 eo[r0 + i, h] = e + (np.abs(out[r0 + i, h]) + e) * HALF[kind] + TINY[kind]
