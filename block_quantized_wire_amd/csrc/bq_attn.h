@@ -12,7 +12,9 @@
 // cores take exactly.  A word of 8 codes becomes 4 registers of 2 operands with 4 ANDs and a
 // shift.  q is scaled by a power of two to just below 2^14 (its numbers that meet the codes four
 // bits higher by 2^-4 more), so binary16 holds it exactly but for numbers 2^-24 below the largest.
-// Codes of values are centred to c - 8: over many tokens the result is small beside the sums of c s
+// Codes of values are centred to c - 8, by a product with -8 or, for binary16 results, before the
+// product (matrix cores cut off what is far below their largest term, which biased long sums of the
+// first form by 2^-17 of a scale): over many tokens the result is small beside the sums of c s
 // and of m, and would be lost in their binary32 rounding.
 // p goes in as one binary16 number where the result is bf16, whose rounding is 8 times as large;
 // for binary16 results as a sum of two (22 bits in all).
@@ -159,13 +161,15 @@ __device__ __forceinline__ h16x8 codes8(uint32_t w) {
         h16x8, u32x4{w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u});
 }
 
-// Codes of the low bits of both half-words as numbers: 1024 + c is a binary16 number with c in its
-// low bits.  v_and_or_b32 takes one constant that is not in a vector register.
-__device__ __forceinline__ uint32_t numbers(uint32_t w) {
-    uint32_t one = 0x64006400u;
+// Codes of the low bits of both half-words, or of the bits above them, as numbers c - Less: 1024 + c is
+// a binary16 number with c in its low bits, 64 + c one with c four bits higher.  v_and_or_b32 takes one
+// constant that is not in a vector register.
+template <bool Above, int Less>
+__device__ __forceinline__ h16x2 numbers(uint32_t w) {
+    uint32_t one = Above ? 0x54005400u : 0x64006400u;
     asm("" : "+v"(one));
-    const h16x2 off{(_Float16)-1024.0f, (_Float16)-1024.0f};
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, (w & 0x000F000Fu) | one) + off);
+    const _Float16 off = (_Float16)(-(Above ? 64.0f : 1024.0f) - Less);
+    return __builtin_bit_cast(h16x2, (w & (Above ? 0x00F000F0u : 0x000F000Fu)) | one) + h16x2{off, off};
 }
 
 // Global-to-LDS load of 16 (4) bytes per lane: lane i's land at lds + 16 i (4 i).
@@ -615,8 +619,11 @@ struct Tokens : State<D, G, F16, 1> {
             u32x4 op;
 #pragma unroll
             for (int tp = 0; tp < 4; ++tp) {
-                const uint32_t w = vw[tp * (D / 64) + j / 4];
-                op[tp] = (j % 4 >= 2 ? w >> 8 : w) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
+                const uint32_t w = vw[tp * (D / 64) + j / 4], x = j % 4 >= 2 ? w >> 8 : w;
+                if constexpr (F16)
+                    op[tp] = __builtin_bit_cast(uint32_t, j & 1 ? numbers<true, 8>(x) : numbers<false, 8>(x));
+                else
+                    op[tp] = x & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
             }
             return __builtin_bit_cast(h16x8, op);
         }
@@ -761,11 +768,10 @@ struct Tokens : State<D, G, F16, 1> {
                 const h16x8 eight = __builtin_bit_cast(h16x8, u32x4{e, e, e, e});
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    if constexpr (F16) {
-                        acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(eight, pl[c], acc[c][j], 0, 0, 0);
+                    if constexpr (F16)
                         acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, pl[c], acc[c][j], 0, 0, 0);
-                    }
-                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(eight, ph[c], acc[c][j], 0, 0, 0);
+                    else
+                        acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(eight, ph[c], acc[c][j], 0, 0, 0);
                     acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
                 }
             }
@@ -806,7 +812,7 @@ struct Tokens : State<D, G, F16, 1> {
         f32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(acc[c][j][i], j & 1 ? 0x1p20f : 0x1p24f, least[j / (NJ / NG)]);
+            o[i] = __builtin_fmaf(acc[c][j][i], F16 ? 1.0f : j & 1 ? 0x1p20f : 0x1p24f, least[j / (NJ / NG)]);
         return o;
     }
 
@@ -1276,9 +1282,9 @@ struct Rows : State<D, G, F16, NC> {
             for (int tp = 0; tp < 4; ++tp) {
                 // D == 64: blocks 2 part and 2 part + 1 of the same words
                 const uint32_t w = x.w[tp] >> (D == 64 ? 8 * part_of + 4 * i : 4 * i);
-                const h16x2 c = __builtin_bit_cast(h16x2, numbers(w));
                 op[tp] = __builtin_bit_cast(
-                    uint32_t, __builtin_elementwise_fma(c, s2[16 * i / G][tp], m2[16 * i / G][tp]));
+                    uint32_t, __builtin_elementwise_fma(numbers<false, 0>(w), s2[16 * i / G][tp],
+                                                        m2[16 * i / G][tp]));
             }
             *reinterpret_cast<u32x4*>(buf + kV + (step_of * NJ + j) * kOperand + lane * 16) = op;
         }

@@ -180,6 +180,19 @@ def test_turns_dealt_out(dim, group, kind, new, window):
     c.check(window=window)
 
 
+def test_long_sums_are_not_biased():
+    """Many tokens of about the same weight: a result is far smaller than its values, and what the sums
+    lose on the way must not add up.  A rounding to binary16 is off by at most 2^-11 of a result, to either
+    side, so the mean of n of them has a deviation of at most 2^-11 of their size by sqrt(3 n)."""
+    for dim, group in ((128, 32), (64, 64), (256, 128)):
+        say(f"attn long sums dim={dim}")
+        c = Case([dim], (21071,), None, 8, 2, dim, group, 64, "f16", q_size=0.1)
+        got, _ = c.check()
+        y = c.want()[0]
+        off = got.cpu().double().numpy() - y
+        assert abs(off.mean()) <= 5 * 2.0 ** -11 * np.sqrt((y * y).mean()) / np.sqrt(3 * y.size)
+
+
 def test_rows_behind_the_last_sequence_are_left():
     for new, extra in ((None, 5), ((3, 8), 7), ((80, 2), 1)):
         c = Case([extra], (50, 90), new, 4, 2, 128, 32, 8, "bf16")
