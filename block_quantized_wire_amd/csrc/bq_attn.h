@@ -1114,6 +1114,7 @@ struct Rows : State<D, G, F16, NC> {
     static constexpr int kBuffer = kB + 64;
     static_assert(NG * T <= 256, "an entry of the keys' scales to a lane");
     static constexpr float kUp = 6.0f;      // p is up to 2^(kRaise + kUp)
+    static constexpr float kApart = -60.0f;
 
     const int32_t* table;
     int wave, step_of, part_of;
@@ -1314,8 +1315,12 @@ struct Rows : State<D, G, F16, NC> {
         const bool raise = this->tops(x, top);
         if (__any(raise || (!F16 && b < k2)))
             new_reference(top, b);
-        const float up = F16 ? kUp : k2 - b + kUp;
-        const float down = F16 ? 1.0f : __builtin_amdgcn_exp2f(b - k2);
+        // A block's values may be smaller than the largest so far by any power of two.  What p takes of it
+        // stays where binary32 holds p and the weights' sum, which does not go by the values: times 2^-60 p
+        // is 0 as a binary16 number.
+        const float apart = F16 ? 0.0f : __builtin_fmaxf(k2 - b, kApart);
+        const float up = apart + kUp;
+        const float down = F16 ? 1.0f : __builtin_amdgcn_exp2f(-apart);
         h16x8 ph[NC], pl[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {

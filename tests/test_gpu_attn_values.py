@@ -1,0 +1,71 @@
+"""Attention over the 4-bit cache where sizes of values differ: blocks of zeros, very small and very
+unequal values, values beyond binary16's range.  Against kv_ref's 64-bit form."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import kv_ref as ref
+from gpu_util import DEV, say, sync
+from test_gpu_attn import Case
+from test_gpu_kv import WIDTHS
+
+import block_quantized_wire_amd as bq
+
+pytestmark = pytest.mark.gpu
+
+
+def places(c, tokens, b=0):
+    """(page, place) of tokens of a sequence."""
+    return [(int(c.table[b, t // c.pool.page]), t % c.pool.page) for t in tokens]
+
+
+def scale_values(c, tokens, by):
+    """The values of these tokens times a power of two (exact, as long as it stays in range)."""
+    for page, place in places(c, tokens):
+        s = c.pool.scales[1][page, :, :, place]
+        c.pool.scales[1][page, :, :, place] = (s.double() * by).to(s.dtype)
+
+
+def near(c, **how):
+    """Like Case.check, with what the header grants small values beside large ones.
+
+    A weight times 2^(6 + k - b) (many rows; b, k: the power of two of a block of 8 tokens, and of the
+    sequence) or times a scale and 2^k (few rows) is a binary16 number, whose steps below 2^-14 are 2^-24, so
+    it is off by 2^-25 at most.  The block's values times 2^b are below 2^15 and the sequence's largest,
+    top, times 2^k is 2^14 or more: that is 2^-25 * 2^15 / 2^6 * top / 2^14 = 2^-30 top a token.  Few rows:
+    codes are up to 8 from the middle and the largest scale times 2^k is 2^6 or more where the weight of the
+    reference is 1: 2^-25 * 8 / 2^6 = 2^-28 of the largest scale a token.  Weights sum to 1 or more then.
+    2^-27 top covers both."""
+    got, lse = c.run(**how)
+    sync()
+    y, l, ey, el = c.want(**how)
+    n = max(c.lens)
+    pairs = c.pool.scales[1].double().numpy()
+    used = np.concatenate([c.table[b, : -(-m // c.pool.page)] for b, m in enumerate(c.lens)])
+    s, m = pairs[used, ..., 0], pairs[used, ..., 1]
+    top = (8 * np.abs(s) + np.abs(m + 8 * s)).max()
+    far = np.abs(got.cpu().double().numpy() - y)
+    assert np.isfinite(far).all()
+    assert (far <= ey + n * 2.0 ** -27 * top).all()
+    seen = np.isfinite(l)
+    found = lse.cpu().double().numpy()
+    assert (found[~seen] == -np.inf).all()
+    assert (np.abs(found - np.where(seen, l, 0))[seen] <= el[seen]).all()
+    return got, lse
+
+
+@pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("new", [(120,), (100, 3)])
+def test_many_rows_of_very_unequal_values(dim, group, new):
+    """Blocks near 2^-90 beside others near 2^60, either first: small values go, weights and
+    log-sum-exps stay."""
+    lens = (150,) if len(new) == 1 else (150, 30)
+    for first, then in ((60, -90), (-90, 60), (0, -80), (-85, 90)):
+        say(f"attn unequal D={dim} G={group} new={new} 2^{first} then 2^{then}")
+        c = Case([dim, group, 2], lens, new, 4, 2, dim, group, 16, "bf16", q_size=1.0)
+        scale_values(c, range(64), 2.0 ** first)
+        scale_values(c, range(64, 150), 2.0 ** then)
+        near(c)
+        near(c, window=70)
