@@ -1115,6 +1115,7 @@ struct Rows : State<D, G, F16, NC> {
     static_assert(NG * T <= 256, "an entry of the keys' scales to a lane");
     static constexpr float kUp = 6.0f;      // p is up to 2^(kRaise + kUp)
     static constexpr float kApart = -60.0f;
+    static constexpr int kNoSize = 200;     // above every block's power of two
 
     const int32_t* table;
     int wave, step_of, part_of;
@@ -1254,7 +1255,8 @@ struct Rows : State<D, G, F16, NC> {
         int b = 0;
         if constexpr (!F16) {
             top = row_max16(top);
-            b = clampi(15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top)), -112, 100);
+            // a block of zeros, or one that no row sees, leaves k as it is
+            b = top == 0 ? kNoSize : clampi(15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top)), -112, 141);
         }
         // a lane scales one token's pair for each of its groups, and the quarter wave shares them
         h16x2 s2[GV][4], m2[GV][4];
@@ -1391,7 +1393,7 @@ struct Rows : State<D, G, F16, NC> {
             x = load(wc, ws, b0 * 8);
         }
         this->load_q(sq, first, rows);
-        k2 = F16 ? 0.0f : 200.0f;
+        k2 = F16 ? 0.0f : (float)kNoSize;
         if (b0 < b1) {
             const int bpp = (int)p.bpp.d;
             unpack(x, lds, b0 * 8);

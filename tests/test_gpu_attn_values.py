@@ -56,6 +56,23 @@ def near(c, **how):
     return got, lse
 
 
+@pytest.mark.parametrize("dim,group,size", [(d, g, -30) for d, g in WIDTHS] +
+                         [(64, 32, -60), (128, 64, -110), (256, 128, -110)])
+def test_values_that_are_all_small(dim, group, size):
+    """Tokens behind a sequence's end and before a window, and a block of zeros, have no size of their
+    own: the small values beside them keep their bits."""
+    for lens, new, window in (((150,), (120,), 0), ((150,), (120,), 61), ((150, 41), (66, 1), 0), ((150,), (17,), 0),
+                              ((150, 41), None, 0)):
+        say(f"attn small values D={dim} G={group} 2^{size} new={new} window={window}")
+        c = Case([dim, group, 1], lens, new, 4, 1, dim, group, 16, "bf16")
+        c.pool.scales[1] = (c.pool.scales[1].double() * 2.0 ** size).to(torch.bfloat16)
+        c.check(window=window)
+        for page, place in places(c, range(40, 48)):
+            c.pool.scales[1][page, :, :, place] = 0
+        c.cache = None
+        c.check(window=window)
+
+
 @pytest.mark.parametrize("dim,group", WIDTHS)
 @pytest.mark.parametrize("new", [(120,), (100, 3)])
 def test_many_rows_of_very_unequal_values(dim, group, new):
