@@ -1084,8 +1084,8 @@ __global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void
 //
 // Values become binary16 numbers here, c s + m in one rounding, so that p needs no scale of each
 // group.  For that the 8 tokens of a block take a power of two 2^b that brings their
-// largest to just below 2^15 (1 in the _f16 kernels, whose values fit); a quarter wave's 8 tokens of
-// p are one block, so p takes 2^(k - b) there, k the least b so far.
+// largest to just below 2^15 (in the _f16 kernels one of 1 or less, where it is larger); a quarter wave's
+// 8 tokens of p are one block, so p takes 2^(k - b) there, k the least b so far.
 //
 // Measured: 8192 rows and tokens, causal, 32 heads on 8 of 128 numbers, bf16, groups of 64, 786 us or 700
 // TFLOP/s of the 1223 of a large product; vector instructions fill 61% of the cycles and products 27%
@@ -1226,6 +1226,36 @@ struct Rows : State<D, G, F16, NC> {
         return (x & 0xFFFFu) == (e & 0xFFFFu) || (x >> 16) == (e >> 16);
     }
 
+    // Whether a value of the block may be 2^15 or more: a scale of 2^10, a least value of 2^14.
+    __device__ __forceinline__ bool large(const Raw& x) const {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 top{0, 0};
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x.t[i] & 0x7FFF7FFFu));
+        return __any(top.x >= 0x6400u || top.y >= 0x7400u);
+    }
+    // The power of two of the block of value codes that this lane has.
+    __device__ __forceinline__ int fit(const Raw& x, int tok) const {
+        // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 and m are within
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const float s = lo16<F16>(x.t[i]), m = hi16<F16>(x.t[i]);
+            const float v = __builtin_fabsf(__builtin_fmaf(8.0f, s, m)) + 8.0f * __builtin_fabsf(s);
+            const int t = tok + step_of * kStep + 8 * g + (r & 7);
+            const bool out = wild(x.t[i]) || !x.ok || t < wg_lo || t >= wg_hi;
+            top = max(top, out ? 0u : __float_as_uint(v));
+        }
+        top = row_max16(top);
+        const int b = 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top));
+        // binary16's own values go as they are unless one passes the range, which a scale that was rounded up
+        // can make of the largest number; a block of zeros, or one that no row sees, leaves k as it is
+        if (F16)
+            return b < 0 ? b : 0;
+        return top == 0 ? kNoSize : clampi(b, -112, 141);
+    }
+
     __device__ __forceinline__ void unpack(const Raw& x, char* buf, int tok) const {
         if (!of_values()) {
             const int h = part_of & 1, w0 = NS == 1 ? (part_of >> 1) * (W / 2) : 0;
@@ -1242,22 +1272,7 @@ struct Rows : State<D, G, F16, NC> {
             }
             return;
         }
-        // the block's largest value: of |m + 8 s| + 8 |s|, which all 16 and m are within
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; !F16 && i < NB; ++i) {
-            const float s = lo16<F16>(x.t[i]), m = hi16<F16>(x.t[i]);
-            const float v = __builtin_fabsf(__builtin_fmaf(8.0f, s, m)) + 8.0f * __builtin_fabsf(s);
-            const int t = tok + step_of * kStep + 8 * g + (r & 7);
-            const bool out = wild(x.t[i]) || !x.ok || t < wg_lo || t >= wg_hi;
-            top = max(top, out ? 0u : __float_as_uint(v));
-        }
-        int b = 0;
-        if constexpr (!F16) {
-            top = row_max16(top);
-            // a block of zeros, or one that no row sees, leaves k as it is
-            b = top == 0 ? kNoSize : clampi(15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top)), -112, 141);
-        }
+        const int b = F16 && !large(x) ? 0 : fit(x, tok);
         // a lane scales one token's pair for each of its groups, and the quarter wave shares them
         h16x2 s2[GV][4], m2[GV][4];
         const int tok_of = tok + step_of * kStep + 8 * g + (r & 7);
@@ -1265,8 +1280,12 @@ struct Rows : State<D, G, F16, NC> {
         S::template unroll<GV>([&](auto gi) {
             constexpr int k = decltype(gi)::value;
             const uint32_t w = wild(x.s[k]) || !seen ? 0u : x.s[k];
-            uint32_t pair = w;
-            if constexpr (!F16) {
+            uint32_t pair;
+            if constexpr (F16) {
+                // b >= -6: a scale or least value loses 2^-25 at most, where the block's largest value is 2^14
+                const _Float16 by = (_Float16)__builtin_ldexpf(1.0f, b);
+                pair = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, w) * h16x2{by, by});
+            } else {
                 const f32x2 two{__builtin_ldexpf(lo16<F16>(w), b), __builtin_ldexpf(hi16<F16>(w), b)};
                 pair = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, h16x2));
             }
@@ -1315,14 +1334,14 @@ struct Rows : State<D, G, F16, NC> {
         }
         float top[NC];
         const bool raise = this->tops(x, top);
-        if (__any(raise || (!F16 && b < k2)))
+        if (__any(raise || b < k2))
             new_reference(top, b);
         // A block's values may be smaller than the largest so far by any power of two.  What p takes of it
         // stays where binary32 holds p and the weights' sum, which does not go by the values: times 2^-60 p
         // is 0 as a binary16 number.
-        const float apart = F16 ? 0.0f : __builtin_fmaxf(k2 - b, kApart);
+        const float apart = __builtin_fmaxf(k2 - b, kApart);
         const float up = apart + kUp;
-        const float down = F16 ? 1.0f : __builtin_amdgcn_exp2f(-apart);
+        const float down = __builtin_amdgcn_exp2f(-apart);
         h16x8 ph[NC], pl[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -1333,7 +1352,7 @@ struct Rows : State<D, G, F16, NC> {
                 pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[c][i], fac[c], -ref));
                 sum += pr[i];
             }
-            l[c] = F16 ? l[c] + sum : __builtin_fmaf(sum, down, l[c]);
+            l[c] = __builtin_fmaf(sum, down, l[c]);
             split8<F16>(pr, ph[c], pl[c]);
         }
 #pragma unroll
@@ -1349,14 +1368,11 @@ struct Rows : State<D, G, F16, NC> {
     }
 
     __device__ __forceinline__ void new_reference(const float (&top)[NC], float b) {
-        float fit = 1.0f;
-        if constexpr (!F16) {
-            b = __builtin_fminf(b, __shfl_xor(b, 16));
-            b = __builtin_fminf(b, __shfl_xor(b, 32));
-            b = __builtin_fminf(b, k2);
-            fit = __builtin_amdgcn_exp2f(b - k2);
-            k2 = b;
-        }
+        b = __builtin_fminf(b, __shfl_xor(b, 16));
+        b = __builtin_fminf(b, __shfl_xor(b, 32));
+        b = __builtin_fminf(b, k2);
+        const float fit = __builtin_amdgcn_exp2f(b - k2);
+        k2 = b;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const float by = this->raised(c, top[c]), both = by * fit;
@@ -1434,10 +1450,9 @@ struct Rows : State<D, G, F16, NC> {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 f32x4 y = acc[c][j];
-                if constexpr (!F16)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        y[i] = __builtin_ldexpf(y[i], (int)-k2);
+                for (int i = 0; i < 4; ++i)
+                    y[i] = __builtin_ldexpf(y[i], (int)-k2);
                 if (whole)
                     put4<F16>(o + 16 * j, y, by);
                 else

@@ -86,3 +86,55 @@ def test_many_rows_of_very_unequal_values(dim, group, new):
         scale_values(c, range(64, 150), 2.0 ** then)
         near(c)
         near(c, window=70)
+
+
+@pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("new", [(120,), (66, 3), (4,)])
+def test_binary16_values_beyond_the_range(dim, group, new):
+    """Finite scales and least values whose 15 s + m is 65536, which binary16 does not hold: rows that do
+    not see the token lose nothing by it, the others have the value itself."""
+    lens = (150,) if len(new) == 1 else (150, 20)
+    first = 149 - new[0] + 1            # place of the sequence's first row
+    for token in (149, first + 2):
+        c = Case([dim, group, 6], lens, new, 4, 2, dim, group, 16, "f16", q_size=0.1)
+        page, place = places(c, [token])[0]
+        codes = np.full((2, dim), 15, np.uint8)
+        codes[:, ::2] = 0
+        c.pool.put(1, page * 16 + place, codes, torch.full((2, dim // group), 8736.0).half(),
+                   torch.full((2, dim // group), -65504.0).half())
+        say(f"attn beyond binary16 D={dim} G={group} new={new} token={token}")
+        near(c)
+
+
+@pytest.mark.parametrize("low", [0.0, -65504.0])
+def test_binary16_rows_of_the_largest_range_are_written_and_attended(low):
+    """What bq_kv_write_i4_f16 makes of rows up to 65504: a scale whose 15 steps pass the type's range."""
+    c = Case([8], (150,), (120,), 4, 2, 128, 64, 16, "f16", q_size=0.1)
+    c.arrays()
+    page, place = places(c, [149])[0]
+    x = torch.full((1, 2, 128), low, dtype=torch.float16, device=DEV)
+    x[..., ::2] = 65504.0
+    k = torch.zeros_like(x)
+    bq.bq_kv_write_i4_f16(k, x, torch.tensor([page * 16 + place], dtype=torch.int32, device=DEV), c.cache)
+    for which, rows in enumerate((k, x)):
+        codes, s, m = ref.quantise(rows.cpu(), 64, "f16")
+        assert which == 0 or float((15 * s.double() + m.double()).max()) > 65504
+        c.pool.put(which, page * 16 + place, codes[0], s[0], m[0])
+    near(c)
+
+
+def test_a_weight_of_zero_beside_a_value_beyond_binary16():
+    """Rows see the token, but its score is so low that its weight is 0."""
+    c = Case([9], (150,), (120,), 4, 2, 64, 32, 16, "f16")
+    page, place = places(c, [10])[0]
+    slot = page * 16 + place
+    # the keys of the token are 0; every other key has a score of some 200 and more
+    c.q = torch.full_like(c.q, 4.0)
+    for which in (0, 1):
+        c.pool.put(which, slot, np.full((2, 64), 15, np.uint8), torch.full((2, 2), 8736.0 if which else 0.0).half(),
+                   torch.full((2, 2), -65504.0 if which else 0.0).half())
+    k = c.pool.scales[0]
+    k[..., 1] = (k[..., 1].float() + 20.0).half()
+    c.pool.scales[0][page, :, :, place] = 0
+    got, _ = near(c)
+    assert float(got.abs().max()) < 100.0
