@@ -684,8 +684,12 @@ struct Tokens : State<D, G, F16, 1> {
         }
     };
 
+    static constexpr float kDown = 18.0f;   // p is up to 2^(kRaise - kDown): 2^30 of them times 2^104 add up
     float mb[NC][NG];
-    float k2, s_lim;          // the power of two of p, largest scale that it is meant for
+    static constexpr int kTop = 15 - (int)(kRaise - kDown);     // scales times 2^k2 are up to 2^kTop
+    static constexpr int kMaxK = 150;
+    int k2;
+    float s_lim;              // largest scale that it is meant for
 
     // 32 tokens from `tok` on.  ok: the 8 tokens' page is there.  mask (uniform): not every row sees
     // every token.  Scales of values that are not finite then go into the score of the rows that
@@ -728,7 +732,7 @@ struct Tokens : State<D, G, F16, 1> {
         float pr[NC][8];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const float ref = R[c] == -__builtin_inff() ? 0.0f : R[c] - k2;
+            const float ref = R[c] == -__builtin_inff() ? 0.0f : R[c] + kDown;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -737,11 +741,16 @@ struct Tokens : State<D, G, F16, 1> {
             }
             l[c] += sum;
         }
+        Src fit = src;      // scales of values as they meet p
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+            if (NG == 1 || 2 * i >= NG)
+                fit.ss[i] = __builtin_ldexpf(fit.ss[i], k2);
         S::template unroll<NG>([&](auto gi) {
             constexpr int k = decltype(gi)::value;
             h16x8 ph[NC], pl[NC];
             float s[8], m[8];
-            src.template v_scales<k>(s, m);
+            fit.template v_scales<k>(s, m);
             if (mask) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -780,25 +789,27 @@ struct Tokens : State<D, G, F16, 1> {
         });
     }
 
-    // Raises the rows' references to their largest scores, and fits 2^k to the largest scale.
+    // Raises the rows' references to their largest scores, and fits 2^k to the largest scale: p times
+    // scale times 2^k is up to 2^15.  The sums of p and of least values do not take 2^k: they hold
+    // whatever the scales are.
     __device__ __forceinline__ void new_reference(const float (&top)[NC], float s_max) {
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1)
             s_max = __builtin_fmaxf(s_max, __shfl_xor(s_max, d));
         float up = 1.0f;
         if (s_max > s_lim) {
-            const int e = clampi(__builtin_amdgcn_frexp_expf(s_max), -93, 107);
-            up = __builtin_amdgcn_exp2f((float)(7 - e) - k2);
-            k2 = (float)(7 - e);
+            const int e = clampi(__builtin_amdgcn_frexp_expf(s_max), kTop - kMaxK, 107);
+            up = __builtin_amdgcn_exp2f((float)(kTop - e - k2));
+            k2 = kTop - e;
             s_lim = __builtin_ldexpf(1.0f, e);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const float by = this->raised(c, top[c]), both = by == 0.0f ? 0.0f : by * up;
-            l[c] *= both;
+            const float by = this->raised(c, top[c]), both = by * up;
+            l[c] *= by;
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                mb[c][k] *= both;
+                mb[c][k] *= by;
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -809,10 +820,12 @@ struct Tokens : State<D, G, F16, 1> {
 
     // The row's result before the division, numbers 16j + 4g .. +3.
     __device__ __forceinline__ f32x4 result(int c, int j, const float (&least)[NG]) const {
+        const float by_even = __builtin_ldexpf(1.0f, (F16 ? 0 : 24) - k2);
+        const float by_odd = __builtin_ldexpf(1.0f, (F16 ? 0 : 20) - k2);
         f32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(acc[c][j][i], F16 ? 1.0f : j & 1 ? 0x1p20f : 0x1p24f, least[j / (NJ / NG)]);
+            o[i] = __builtin_fmaf(acc[c][j][i], j & 1 ? by_odd : by_even, least[j / (NJ / NG)]);
         return o;
     }
 
@@ -923,7 +936,7 @@ struct Tokens : State<D, G, F16, 1> {
         begin(ring, from + 4 * wave, to < end ? to : end);
         this->range(sq, first, 16, rows, lo, hi);
         this->load_q(sq, first, rows);
-        k2 = 0.0f;
+        k2 = kMaxK;
         s_lim = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -949,7 +962,7 @@ struct Tokens : State<D, G, F16, 1> {
             for (int j = 0; j < NJ; ++j)
                 *reinterpret_cast<f32x4*>(part + 16 * j + 4 * g) = result(c, j, least);
             if (g == 0)
-                *reinterpret_cast<f32x2*>(ml + 2 * (wave * 16 + r)) = f32x2{R[c] - k2, sum};
+                *reinterpret_cast<f32x2*>(ml + 2 * (wave * 16 + r)) = f32x2{R[c] + kDown, sum};
             __syncthreads();
             const int mine = threadIdx.x >> 4, seg = threadIdx.x & 15;
             const int row = first + 16 * c + mine;

@@ -89,6 +89,38 @@ def test_many_rows_of_very_unequal_values(dim, group, new):
 
 
 @pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("new", [None, (4,), (3, 8)])
+def test_few_rows_of_very_unequal_values(dim, group, new):
+    lens = (150, 30) if new is not None and len(new) > 1 else (150,)
+    for first, then in ((60, -90), (-90, 60), (0, -80), (-85, 90)):
+        say(f"attn unequal D={dim} G={group} new={new} 2^{first} then 2^{then}")
+        c = Case([dim, group, 3], lens, new, 4, 2, dim, group, 16, "bf16", q_size=1.0)
+        scale_values(c, range(128), 2.0 ** first)       # a turn of the four waves, each of which has both
+        scale_values(c, range(128, 150), 2.0 ** then)
+        near(c)
+    # long enough that turns are dealt out and joined
+    c = Case([dim, group, 4], (3000,), new and (4,), 8, 1, dim, group, 64, "bf16", q_size=1.0)
+    scale_values(c, range(500, 1700), 2.0 ** -85)
+    scale_values(c, range(1700, 3000), 2.0 ** 80)
+    near(c)
+
+
+def test_scales_that_are_far_below_their_least_values():
+    """Groups of nearly equal numbers, some exactly equal: sums of least values stay in range whatever the
+    power of two of the scales."""
+    for kind in ("bf16", "f16"):
+        for new in (None, (4,), (90,)):
+            say(f"attn tiny scales {kind} new={new}")
+            c = Case([5], (300,), new, 4, 2, 128, 64, 16, kind, q_size=1.0)
+            by = 2.0 ** -95 if kind == "bf16" else 0.0
+            v = c.pool.scales[1]
+            v[..., 0] = (v[..., 0].double() * by).to(v.dtype)
+            if kind == "bf16":
+                v[..., 1] = (v[..., 1].double() * 2.0 ** 40).to(v.dtype)
+            near(c)
+
+
+@pytest.mark.parametrize("dim,group", WIDTHS)
 @pytest.mark.parametrize("new", [(120,), (66, 3), (4,)])
 def test_binary16_values_beyond_the_range(dim, group, new):
     """Finite scales and least values whose 15 s + m is 65536, which binary16 does not hold: rows that do
