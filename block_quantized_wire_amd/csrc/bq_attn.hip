@@ -36,9 +36,10 @@ AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, i
         // 8192 40 and 65, of 2048 23 and 22; 32 of 1000 to 8192 47 and 63, of 8192 67 and 66, of 2048 31
         // and 22; 64 of 4096 68 and 51.
         const int64_t long_by = (384 - base) * max_len * (dim == 256 || dim / group >= 4 ? 2 : 1);
-        if (seqs <= attn::kMaxDealt && base < 384 && long_by > (int64_t)1 << 19) {
+        // The kernels count turns in 32 bits.
+        const int64_t turns = base * ((max_len + 127) / 128 + 1);
+        if (seqs <= attn::kMaxDealt && base < 384 && long_by > (int64_t)1 << 19 && turns < (int64_t)1 << 31) {
             const int64_t most = kCus * attn::tokens_groups(dim, group, true);
-            const int64_t turns = base * ((max_len + 127) / 128 + 1);
             p.dealt = (int)(turns < most ? turns : most);
             p.ws_bytes = p.dealt * (int64_t)(2 * 16 * 4) * (dim + 2) + 4 * (2 * attn::kMaxDealt + 1);
         }
