@@ -261,6 +261,10 @@ struct State {
     __device__ __forceinline__ void load_q(const Seq& sq, int first, int rows) {
         full_lo = 0;
         full_hi = 1 << 30;
+        // Rows of q are scaled to just below 2^14, those below 2^least to less: they go without the bits that
+        // this leaves them.  Where q and the scale are both very small it keeps fac a normal number: a masked
+        // score is -inf * fac.
+        const int least = max(-100, -135 - __builtin_amdgcn_frexp_expf(p.scale2));
         // a negative scale is that of -q
         const float sign = p.scale2 < 0.0f ? -1.0f : p.scale2 > 0.0f ? 1.0f : 0.0f;
 #pragma unroll
@@ -284,8 +288,7 @@ struct State {
                     top = __builtin_fmaxf(top, __builtin_fabsf(f[8 * k + i]));
             }
             top = quarter_max(top);
-            // rows below 2^-100 go without the bits that this leaves them
-            const int e = clampi(__builtin_amdgcn_frexp_expf(top), -100, 128);
+            const int e = clampi(__builtin_amdgcn_frexp_expf(top), least, 128);
             const float by = sign * __builtin_ldexpf(1.0f, 14 - e);
             fac[c] = sign == 0.0f ? 1.0f : __builtin_ldexpf(__builtin_fabsf(p.scale2), 10 + e);
             float bad = 0.0f;
