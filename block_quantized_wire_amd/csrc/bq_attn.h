@@ -133,9 +133,10 @@ __device__ __forceinline__ float quarter_max(float v) {
     return __builtin_fmaxf(v, __shfl_xor(v, 32));
 }
 
-// Which rows of q and which tokens a sequence has; brought inside the arrays.
+// Which rows of q and which tokens a sequence has; brought inside the arrays.  at0: the first row's
+// place, which rows beyond max_q move too; rows further in front than max_q (2^20 at most) see the same.
 struct Seq {
-    int row0, n, len;
+    int row0, n, len, at0;
 };
 __device__ __forceinline__ Seq seq_of(const AttnI4& a, int b) {
     Seq s;
@@ -143,14 +144,14 @@ __device__ __forceinline__ Seq seq_of(const AttnI4& a, int b) {
         s.row0 = clampi(a.starts[b], 0, a.rows);
         const int end = clampi(a.starts[b + 1], s.row0, a.rows);
         s.n = end - s.row0;
-        if (s.n > a.max_q)
-            s.n = a.max_q;
     } else {
         s.row0 = b;
         s.n = b < a.rows ? 1 : 0;
     }
     const int64_t room = (int64_t)a.table_cols * a.c.page_size;
     s.len = clampi(a.lens[b], 0, room < a.max_len ? (int)room : a.max_len);
+    s.at0 = max(s.len - s.n, -(1 << 21));
+    s.n = min(s.n, a.max_q);
     return s;
 }
 
@@ -252,9 +253,9 @@ struct State {
     // The tokens that rows [first, first + 16 NC) of a sequence see: [lo, hi).
     __device__ __forceinline__ void range(const Seq& sq, int first, int n, int rows, int& from,
                                           int& to) const {
-        const int last = (first + n < rows ? first + n : rows) - 1, at0 = sq.len - sq.n;
-        to = first >= rows ? 0 : p.a.causal ? clampi(at0 + p.share.div(last) + 1, 0, sq.len) : sq.len;
-        from = p.a.window > 0 ? clampi(at0 + p.share.div(first) + 1 - p.a.window, 0, to) : 0;
+        const int last = (first + n < rows ? first + n : rows) - 1;
+        to = first >= rows ? 0 : p.a.causal ? clampi(sq.at0 + p.share.div(last) + 1, 0, sq.len) : sq.len;
+        from = p.a.window > 0 ? clampi(sq.at0 + p.share.div(first) + 1 - p.a.window, 0, to) : 0;
     }
 
     // Rows of q of this wave: `first` is the first of them among the sequence's rows.
@@ -318,7 +319,7 @@ struct State {
                 }
                 q[c][k] = __builtin_bit_cast(h16x8, o);
             }
-            const int at = sq.len - sq.n + qi;      // the row's place
+            const int at = sq.at0 + qi;     // the row's place
             seen_hi[c] = p.a.causal && in ? (at + 1 < sq.len ? at + 1 : sq.len) : sq.len;
             seen_lo[c] = p.a.window > 0 && in && at + 1 - p.a.window > 0 ? at + 1 - p.a.window : 0;
             if (!in) {      // sees what its wave sees
@@ -526,7 +527,7 @@ __device__ __forceinline__ void split_blocks(int lo, int hi, int split, const Di
 constexpr int kTurn = 16;       // blocks of 8 tokens
 __device__ __forceinline__ int turns_of(const AttnI4& a, int b) {
     const Seq s = seq_of(a, b);
-    const int first = s.len - s.n + 1 - a.window;       // the first row's first token, under a window
+    const int first = s.at0 + 1 - a.window;     // the first row's first token, under a window
     const int lo = a.window > 0 && first > 0 ? first : 0;
     const int blocks = (s.len + 7) / 8 - lo / 32 * 4;
     return s.n > 0 && blocks > 0 ? (blocks + kTurn - 1) / kTurn : 0;

@@ -99,7 +99,7 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  * (max_q is then taken as 1).  lse: float[rows][heads] or NULL.
  * max_q, max_len: at least every n_b and lens[b]; 0 <= lens[b].  What the arrays hold beyond
  * that is brought inside: lens to [0, min(max_len, table_cols * page_size)], rows of a sequence
- * beyond max_q are not computed, and the tokens of a page outside [0, pages) are seen by no row.
+ * beyond max_q are not computed (the others stay in their places), and the tokens of a page outside [0, pages) are seen by no row.
  * heads is a multiple of cache->heads, at most 64 times as many; seqs, max_q <= 2^20, rows *
  * heads < 2^31, max_len < 2^30 (else BQ_ERR_SIZE).  With n = max_q * heads / cache->heads rows to a
  * sequence and head of the cache, seqs * cache->heads * ceil(n / 16) is below 2^24 for n <= 64, and
