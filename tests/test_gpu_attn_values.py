@@ -170,3 +170,29 @@ def test_a_weight_of_zero_beside_a_value_beyond_binary16():
     c.pool.scales[0][page, :, :, place] = 0
     got, _ = near(c)
     assert float(got.abs().max()) < 100.0
+
+
+@pytest.mark.parametrize("n", [3000, 1 << 22])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (256, 128)])
+def test_long_sums_of_the_largest_values_stay_in_range(dim, group, n):
+    """Scores of 0 and values of 2^100.  Sums of n equal terms in binary32, 32 tokens or more to a step, are off
+    by 2^-24 a step: 2^-7 for 2^22 tokens, as is the sum of the weights."""
+    pages, size = 4, 256
+    codes = torch.zeros((pages, 1, size, dim // 2), dtype=torch.uint8, device=DEV)
+    scales = [torch.zeros((pages, 1, dim // group, size, 2), dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    scales[1][..., 1] = 2.0 ** 100
+    cache = bq.KvI4(codes, codes.clone(), *scales, group=group)
+    cols = -(-n // size)
+    table = (torch.arange(cols, dtype=torch.int32, device=DEV) % pages)[None].contiguous()
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    for rows in (1, 80):
+        say(f"attn largest values D={dim} n={n} rows={rows}")
+        q = torch.ones((rows, 1, dim), dtype=torch.bfloat16, device=DEV)
+        out, lse = torch.empty_like(q), torch.empty((rows, 1), device=DEV)
+        starts = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+        need = bq.bq_attn_i4_ws_bytes(1, rows, rows, n, 1, 1, dim)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        bq.bq_attn_i4(q, cache, table, lens, out, starts=starts, max_q=rows, max_len=n, causal=False, lse=lse, ws=ws)
+        sync()
+        assert ((out.float() * 2.0 ** -100 - 1).abs() < 2.0 ** -5).all()
+        assert ((lse.double() - float(np.log(n))).abs() < 2.0 ** -6).all()
