@@ -1101,7 +1101,8 @@ __global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void
 // waves unpack values, the other four keys and their scales.
 //
 // Values become binary16 numbers here, c s + m in one rounding, so that p needs no scale of each
-// group.  For that the 8 tokens of a block take a power of two 2^b that brings their
+// group; in the _f16 kernels a second one has what that leaves, or their results would be 40% farther from
+// 64 bits than few rows' are (a third product: 8% to 14% of a call).  For that the 8 tokens of a block take a power of two 2^b that brings their
 // largest to just below 2^15 (in the _f16 kernels one of 1 or less, where it is larger); a quarter wave's
 // 8 tokens of p are one block, so p takes 2^(k - b) there, k the least b so far.
 //
@@ -1127,7 +1128,8 @@ struct Rows : State<D, G, F16, NC> {
     // a buffer: operands of k [step][h][w], of v [step][j], scale and least value of k [2][group][T],
     // then b and whether the page is there for each block of 8 tokens
     static constexpr int kV = NS * 2 * W * kOperand;
-    static constexpr int kS = kV + NS * NJ * kOperand;
+    static constexpr int kLow = NS * NJ * kOperand;     // _f16: what the operands of v leave of the values, behind them
+    static constexpr int kS = kV + (F16 ? 2 : 1) * kLow;
     static constexpr int kB = kS + 2 * NG * T * 4;
     static constexpr int kBuffer = kB + 64;
     static_assert(NG * T <= 256, "an entry of the keys' scales to a lane");
@@ -1155,6 +1157,9 @@ struct Rows : State<D, G, F16, NC> {
         }
         __device__ __forceinline__ h16x8 v(int j) const {
             return *reinterpret_cast<const h16x8*>(buf + kV + (sub * NJ + j) * kOperand + lane * 16);
+        }
+        __device__ __forceinline__ h16x8 v_low(int j) const {
+            return *reinterpret_cast<const h16x8*>(buf + kV + kLow + (sub * NJ + j) * kOperand + lane * 16);
         }
         __device__ __forceinline__ void eight(int which, int k, float (&s)[8]) const {
             const float* at = reinterpret_cast<const float*>(buf + kS) + (which * NG + k) * T + sub * 32 + 8 * g;
@@ -1317,16 +1322,24 @@ struct Rows : State<D, G, F16, NC> {
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
             const int j = part_of * VB + i;
-            u32x4 op;
+            u32x4 op, low;
 #pragma unroll
             for (int tp = 0; tp < 4; ++tp) {
                 // D == 64: blocks 2 part and 2 part + 1 of the same words
                 const uint32_t w = x.w[tp] >> (D == 64 ? 8 * part_of + 4 * i : 4 * i);
-                op[tp] = __builtin_bit_cast(
-                    uint32_t, __builtin_elementwise_fma(numbers<false, 0>(w), s2[16 * i / G][tp],
-                                                        m2[16 * i / G][tp]));
+                const h16x2 c = numbers<false, 0>(w), sc = s2[16 * i / G][tp], le = m2[16 * i / G][tp];
+                const h16x2 v = __builtin_elementwise_fma(c, sc, le);
+                op[tp] = __builtin_bit_cast(uint32_t, v);
+                if constexpr (F16) {
+                    const f32x2 rest{__builtin_fmaf((float)c.x, (float)sc.x, (float)le.x) - (float)v.x,
+                                     __builtin_fmaf((float)c.y, (float)sc.y, (float)le.y) - (float)v.y};
+                    low[tp] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, h16x2));
+                }
             }
-            *reinterpret_cast<u32x4*>(buf + kV + (step_of * NJ + j) * kOperand + lane * 16) = op;
+            char* at = buf + kV + (step_of * NJ + j) * kOperand + lane * 16;
+            *reinterpret_cast<u32x4*>(at) = op;
+            if constexpr (F16)
+                *reinterpret_cast<u32x4*>(at + kLow) = low;
         }
         if (part_of == 0 && r == 0)
             *reinterpret_cast<f32x2*>(buf + kB + 8 * (step_of * 4 + g)) =
@@ -1378,8 +1391,10 @@ struct Rows : State<D, G, F16, NC> {
             const h16x8 o = src.v(j);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                if constexpr (F16)
+                if constexpr (F16) {
                     acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, pl[c], acc[c][j], 0, 0, 0);
+                    acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(src.v_low(j), ph[c], acc[c][j], 0, 0, 0);
+                }
                 acc[c][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o, ph[c], acc[c][j], 0, 0, 0);
             }
         }

@@ -86,10 +86,10 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  * Scores, softmax and sums are in binary32; q is exact but for numbers 2^-24 below the largest of
  * their row.  Before the product with the values, exp(score_t - lse) is held to half a step of
  * binary16 (2^-11 relative; in the _f16 calls 2^-21), and so is v_t where a call has many rows.
- * In the _f16 calls v_t may be beyond binary16's range; it is read back as an infinity, but counts as what it
- * is here.  Values of v that are 2^-16 of the largest of their sequence and head or less lose
- * further bits, the smaller the more; weights and lse do not go by the values, whose scales and
- * least values are at most 2^100.  A NaN or an infinity in a row of q makes every value
+ * In the _f16 calls v_t may be beyond binary16's range; it is read back as an infinity, but counts as what
+ * it is here.  Values of v that are 2^-16 of the largest of their sequence and head or less lose further
+ * bits, the smaller the more; weights and lse do not go by the values, whose scales and least values are at
+ * most 2^100.  A NaN or an infinity in a row of q makes every value
  * of that row and head NaN, one in the scales of a token does not reach rows that do not see it.
  * The same call gives the same bits.
  *

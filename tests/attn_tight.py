@@ -1,4 +1,4 @@
-"""A closer bound than kv_ref's on attention of few rows over a binary16 cache, whose values are exact."""
+"""Closer bounds than kv_ref's on attention over a binary16 cache, whose values are held to 2^-22."""
 from __future__ import annotations
 
 import math
@@ -47,6 +47,40 @@ def attend(pool, q, table, lens, scale, held=None):
     return out, eo
 
 
+def attend_rows(pool, q, table, n, scale, held=None):
+    """out and its bound for many rows of one sequence, each of which sees all n tokens.  held: a rounding of
+    the values, planted.
+
+    Scores, weights and sums as above.  A value is two binary16 numbers: 2^-22 of it, or 2^-25 where the second
+    is below 2^-14.  A weight times 2^6 is two as well: 2^-22 of it, or 2^-25, 2^-31 of the weight of the
+    reference, which the weights' sum is not below; the product of the second ones, 2^-22 of the whole, is left out."""
+    rows, heads, dim = q.shape
+    share = heads // pool.heads
+    x = q.double().numpy()
+    out, eo = np.zeros((rows, heads, dim)), np.zeros((rows, heads, dim))
+    tok = np.arange(n)
+    slot = np.asarray(table)[tok // pool.page].astype(np.int64) * pool.page + tok % pool.page
+    kc, ks, km = pool.get(0, slot)
+    vc, vs, vm = pool.get(1, slot)
+    for h in range(heads):
+        c = h // share
+        k, v = kc[:, c] * ks[:, c] + km[:, c], vc[:, c] * vs[:, c] + vm[:, c]
+        if held is not None:
+            v = held(v)
+        for i in range(rows):
+            a = x[i, h]
+            s = scale * (k @ a)
+            size = abs(scale) * ((kc[:, c] * np.abs(ks[:, c]) + np.abs(km[:, c])) @ np.abs(a))
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            out[i, h] = w @ v
+            off = ULP * ((dim + 16) * size + np.abs(s) + np.abs(s - s.max()) + 4)
+            rel = (w * (off + (w * off).sum() + 3 * 2.0 ** -22 + ULP * (n / 8 + 32)))[:, None]
+            e = (rel * np.abs(v) + w[:, None] * 2.0 ** -25 + 2.0 ** -31 * np.abs(v)).sum(0)
+            eo[i, h] = e + (np.abs(out[i, h]) + e) * 2.0 ** -11 + 2.0 ** -25
+    return out, eo
+
+
 def binary16(x):
     return x.astype(np.float16).astype(np.float64)
 
@@ -54,3 +88,7 @@ def binary16(x):
 def case(make, dim, group, n):
     """Scores of about 0, so that their own rounding is small beside what is looked for."""
     return make([dim, group, n], (n,), None, 4, 2, dim, group, 16, "f16", q_size=2.0 ** -9)
+
+
+def case_rows(make, dim, group, n):
+    return make([dim, group, n, 1], (n,), (40,), 4, 2, dim, group, 16, "f16", q_size=2.0 ** -9)

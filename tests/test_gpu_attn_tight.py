@@ -1,4 +1,5 @@
-"""Few rows: over a binary16 cache weights to 2^-21 and values as they are; long sums without a bias."""
+"""Over a binary16 cache weights to 2^-21 and values to 2^-22 or as they are, for few rows and many; long sums
+of bf16 without a bias."""
 from __future__ import annotations
 
 import numpy as np
@@ -20,6 +21,18 @@ def test_weights_and_values_of_few_rows_are_not_cut(dim, group, n):
     got, _ = c.run()
     sync()
     y, e = attn_tight.attend(c.pool, c.q.cpu(), c.table, c.lens, dim ** -0.5)
+    far = np.abs(got.cpu().double().numpy() - y)
+    assert (far <= e).all(), float((far / e).max())
+
+
+@pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("n", [1, 33, 200, 1500])
+def test_weights_and_values_of_many_rows_are_not_cut(dim, group, n):
+    say(f"attn tight many rows D={dim} G={group} n={n}")
+    c = attn_tight.case_rows(Case, dim, group, n)
+    got, _ = c.run(causal=False)
+    sync()
+    y, e = attn_tight.attend_rows(c.pool, c.q.cpu(), c.table[0], n, dim ** -0.5)
     far = np.abs(got.cpu().double().numpy() - y)
     assert (far <= e).all(), float((far / e).max())
 
