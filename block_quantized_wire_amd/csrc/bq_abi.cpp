@@ -1475,7 +1475,8 @@ bq_status attn_i4(const uint16_t* q, int64_t ldq, int64_t hsq, const bq_kv_i4* c
     BQ_TRY(check_kv(cache));
     const bq_kv_i4& c = *cache;
     BQ_TRY(check_attn_sizes(seqs, rows, max_q, max_len, heads, c.heads));
-    if (table_cols < 0 || table_cols > kMaxLen || window < 0 || !std::isfinite(scale))
+    // times log2(e) it has to be finite; a NaN is refused too
+    if (table_cols < 0 || table_cols > kMaxLen || window < 0 || !(std::fabs(scale) <= 0x1p126f))
         return BQ_ERR_SIZE;
     if (seqs == 0 || rows == 0 || max_q == 0)
         return BQ_OK;

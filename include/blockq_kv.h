@@ -79,7 +79,7 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  *   out_d = bf16_rne( sum over t of exp(score_t - lse) * v_td ).
  * A row at place p sees tokens [0, lens[b]); with causal != 0 those up to p; with window > 0
  * those after p - window.  A row that sees nothing becomes 0, its lse -inf.  Rows of no
- * sequence are not written.  scale is finite (else BQ_ERR_SIZE); where |scale| times a number of
+ * sequence are not written.  |scale| is at most 2^126 (else BQ_ERR_SIZE); where |scale| times a number of
  * q passes 2^117, that row and head may become NaN.  Tokens that a row does not see have no effect on it, whatever their
  * codes and scales hold (but for the bits that much larger scales of v cost, see below).
  *

@@ -2,6 +2,8 @@
 is launched."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 
 import block_quantized_wire_amd as bq
@@ -29,3 +31,17 @@ def test_turns_that_are_dealt_out_can_be_counted():
                     assert size(1, 1, 1, max_len, base, base, dim) == 0
                 else:
                     assert size(1, 1, 1, max_len, base, base, dim) > 0
+
+
+@pytest.mark.parametrize("name", ["bq_attn_i4", "bq_attn_i4_f16"])
+def test_scales_whose_product_with_log2_e_is_not_finite(name):
+    """|scale| up to 2^126 is taken; beyond it every row that sees something would be NaN."""
+    pool = bq._KvI4(16, 32, 48, 64, 2048, 1024, 128, 64, 10, 16, 2, 128, 64)
+
+    def call(scale):        # no sequence: the arguments are looked at, and no pointer is read
+        return getattr(bq.lib, name)(None, 0, 0, ctypes.addressof(pool), None, 0, 0, None, None, 0, 0, 0, 0, 4, 1, 0,
+                                     scale, None, 0, 0, None, None, 0, 0)
+    for scale in (2.0 ** 126, -2.0 ** 126, 0.0, 1e-45):
+        assert call(scale) == 0
+    for scale in (2.0 ** 126 * (1 + 2.0 ** -23), -2.0 ** 127, 3.4e38, float("inf"), -float("inf"), float("nan")):
+        assert call(scale) == 2
