@@ -102,28 +102,6 @@ __device__ __forceinline__ uint32_t bcast_u(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + Lane, 0xF, 0xF, true);
 }
 
-template <bool F16>
-__device__ __forceinline__ float lo16(uint32_t w) {
-    if constexpr (F16)
-        return (float)__builtin_bit_cast(h16x2, w).x;
-    else
-        return bf16_lo(w);
-}
-template <bool F16>
-__device__ __forceinline__ float hi16(uint32_t w) {
-    if constexpr (F16)
-        return (float)__builtin_bit_cast(h16x2, w).y;
-    else
-        return bf16_hi(w);
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (F16)
-        return __builtin_bit_cast(uint32_t, h16x2{(_Float16)a, (_Float16)b});
-    else
-        return pack_bf16x2(a, b);
-}
-
 // Sum, maximum over the four lanes that hold a row of q.
 __device__ __forceinline__ float quarter_sum(float v) {
     v += __shfl_xor(v, 16);

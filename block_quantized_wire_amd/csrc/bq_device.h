@@ -149,6 +149,29 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float f[8]) {
                  pack_bf16x2(f[6], f[7])};
 }
 
+// Either type: the low and the high number of a word, and two numbers rounded into one.
+template <bool F16>
+__device__ __forceinline__ float lo16(uint32_t w) {
+    if constexpr (F16)
+        return (float)__builtin_bit_cast(h16x2, w).x;
+    else
+        return bf16_lo(w);
+}
+template <bool F16>
+__device__ __forceinline__ float hi16(uint32_t w) {
+    if constexpr (F16)
+        return (float)__builtin_bit_cast(h16x2, w).y;
+    else
+        return bf16_hi(w);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (F16)
+        return __builtin_bit_cast(uint32_t, h16x2{(_Float16)a, (_Float16)b});
+    else
+        return pack_bf16x2(a, b);
+}
+
 // ---- DPP row reductions (16 lanes) -----------------------------------------------------
 
 template <int Ctrl>

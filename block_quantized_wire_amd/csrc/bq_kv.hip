@@ -33,28 +33,6 @@ struct KvArgs {
     int64_t units;         // rows of one token and head, tokens in whole eights
 };
 
-template <bool F16>
-__device__ __forceinline__ float lo16(uint32_t w) {
-    if constexpr (F16)
-        return (float)__builtin_bit_cast(h16x2, w).x;
-    else
-        return bf16_lo(w);
-}
-template <bool F16>
-__device__ __forceinline__ float hi16(uint32_t w) {
-    if constexpr (F16)
-        return (float)__builtin_bit_cast(h16x2, w).y;
-    else
-        return bf16_hi(w);
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (F16)
-        return __builtin_bit_cast(uint32_t, h16x2{(_Float16)a, (_Float16)b});
-    else
-        return pack_bf16x2(a, b);
-}
-
 // IEEE minimum and maximum (a NaN stays) over L of the 8 lanes of a row.
 template <int L>
 __device__ __forceinline__ void lanes_min_max(float& lo, float& hi) {
