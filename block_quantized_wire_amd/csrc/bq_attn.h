@@ -1249,12 +1249,13 @@ struct Rows : State<D, G, F16, NC> {
             top = max(top, out ? 0u : __float_as_uint(v));
         }
         top = row_max16(top);
-        const int b = 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(top));
+        // past binary32's range: below 2^133
+        const int b = 15 - (top < 0x7F800000u ? __builtin_amdgcn_frexp_expf(__uint_as_float(top)) : 133);
         // binary16's own values go as they are unless one passes the range, which a scale that was rounded up
         // can make of the largest number; a block of zeros, or one that no row sees, leaves k as it is
         if (F16)
             return b < 0 ? b : 0;
-        return top == 0 ? kNoSize : clampi(b, -112, 141);
+        return top == 0 ? kNoSize : min(b, 141);
     }
 
     __device__ __forceinline__ void unpack(const Raw& x, char* buf, int tok) const {

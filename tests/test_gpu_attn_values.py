@@ -172,6 +172,24 @@ def test_a_weight_of_zero_beside_a_value_beyond_binary16():
     assert float(got.abs().max()) < 100.0
 
 
+@pytest.mark.parametrize("dim,group", WIDTHS)
+@pytest.mark.parametrize("new", [(120,), (4,)])
+def test_unseen_values_as_large_as_bf16_holds(dim, group, new):
+    """The last token's scales and least values are finite, its values are not: rows that do not see it are
+    finite, and their log-sum-exps are right."""
+    for scale, least in ((1.5 * 2.0 ** 127, -2.0 ** 127), (2.0 ** 124, 1.5 * 2.0 ** 127), (2.0 ** 110, 0.0)):
+        say(f"attn largest unseen values D={dim} G={group} new={new} {scale}")
+        c = Case([dim, group, 10], (150,), new, 4, 2, dim, group, 16, "bf16", q_size=1.0)
+        page, place = places(c, [149])[0]
+        c.pool.scales[1][page, :, :, place, 0] = scale
+        c.pool.scales[1][page, :, :, place, 1] = least
+        got, lse = c.run()
+        sync()
+        _, l, _, el = c.want()
+        assert torch.isfinite(got[:-1]).all()
+        assert (np.abs(lse.cpu().double().numpy() - l)[:-1] <= el[:-1]).all()
+
+
 @pytest.mark.parametrize("n", [3000, 1 << 22])
 @pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (256, 128)])
 def test_long_sums_of_the_largest_values_stay_in_range(dim, group, n):
