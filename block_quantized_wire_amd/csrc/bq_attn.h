@@ -531,7 +531,8 @@ struct Deal {
 };
 
 // Workgroups of few rows that a compute unit holds.
-// Their registers decide: a spilled one would be loaded behind the ring and drain it.
+// Their registers decide: one that is spilled in the walk would be loaded behind the ring and drain it.  (Heads of
+// 256 in groups of 64, dealt out, reload one a segment, outside the walk.)
 constexpr int tokens_groups(int dim, int group, bool dealt) {
     return dim == 64 ? (dealt ? 3 : 4) : dim == 128 && group >= 64 ? 3 : dim == 256 && group == 32 ? 1 : 2;
 }
@@ -540,7 +541,8 @@ constexpr int tokens_groups(int dim, int group, bool dealt) {
 //
 // Each wave takes every fourth step of the workgroup's tokens and keeps to itself: a ring of
 // `Depth` steps in LDS, filled by global-to-LDS loads (16 bytes a lane, in the cache's own order),
-// so that the next steps are on their way without a register; no barriers until the waves'
+// so that the next steps (one at a width of 128 in groups of 64 or 128, where three workgroups share the LDS) are
+// on their way without a register; no barriers until the waves'
 // results meet.
 // Chunks of 16 bytes are permuted within a block so that neither operand's reads meet a
 // bank conflict.  Scales: one word or a few to a lane of a quarter wave, broadcast as DPP operands.
@@ -550,7 +552,7 @@ constexpr int tokens_groups(int dim, int group, bool dealt) {
 // as the card holds at once, each of which takes its run of turns through one unit (a sequence,
 // tile and head) or several; only units that workgroups share leave partial results.
 //
-// Measured, one row, 64 heads on 8 of 128 numbers, bf16: 32 sequences of 701 to 8192 tokens (132 MB) 36.6 us
+// Measured, one row, 64 heads on 8 of 128 numbers, bf16: 32 sequences of 701 to 8192 tokens (132 MB) 37.3 us
 // and 6 of joining, dealt out, 64 as a workgroup to each unit; one of 131071 (151 MB) 39 and 6.  Of a large copy's
 // 5.1 TB/s that is 75%: the first loads of a launch and the last sums take about 6 us.  Vector
 // instructions fill 38% to 45% of the cycles, products 10%.
@@ -1084,7 +1086,7 @@ __global__ __launch_bounds__(kThreads, (Tokens<D, G, F16, Dealt>::kGroups)) void
 // largest to just below 2^15 (in the _f16 kernels one of 1 or less, where it is larger); a quarter wave's
 // 8 tokens of p are one block, so p takes 2^(k - b) there, k the least b so far.
 //
-// Measured: 8192 rows and tokens, causal, 32 heads on 8 of 128 numbers, bf16, groups of 64, 786 us or 700
+// Measured: 8192 rows and tokens, causal, 32 heads on 8 of 128 numbers, bf16, groups of 64, 792 us or 694
 // TFLOP/s of the 1223 of a large product; vector instructions fill 61% of the cycles and products 27%
 // of them (32 of 197 in a step of 32 rows and 32 tokens; 64 bring scales and least values into the
 // scores).  LDS instructions fill 31%, without a bank conflict.

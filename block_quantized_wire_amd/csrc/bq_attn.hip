@@ -18,8 +18,8 @@ AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, i
     AttnPlan p{};
     const int64_t m = max_q * (heads / kv_heads);       // rows of one sequence and cache head
     // Up to 64 rows the waves share the tokens, beyond them the tokens' operands (16 sequences of
-    // 4096 tokens, 8 heads of 128 numbers: 64 rows 44-50 us against 63, 96 rows 69 against 76, 128 rows 88
-    // against 80; 2 of 16384, 128 rows: 60 against 48).  Beyond 128 rows a wave has 32 of them (256 rows
+    // 4096 tokens, 8 heads of 128 numbers, bf16: 64 rows 44-50 us against 63, 96 rows 69 against 76, 128 rows 88
+    // against 80; 2 of 16384, 128 rows: 60 against 48; from 65 to 96 rows the tokens' sharing is up to 10% faster).  Beyond 128 rows a wave has 32 of them (256 rows
     // of 16 x 4096 tokens: 147 us, with 16 rows 176; 128 rows: 110 against 88); at a width of 256
     // their results alone would be half of its registers.
     p.by_rows = m > 64;

@@ -183,7 +183,7 @@ struct AttnPlan {
     int tiles, splits, dealt;
     int64_t ws_bytes;
 };
-// Of the groups, 64 takes the largest workspace.
+// The workspace goes by the group too: 32 is dealt out sooner, 64 to more workgroups.
 AttnPlan attn_plan(int64_t seqs, int64_t rows, int64_t max_q, int64_t max_len, int heads,
                    int kv_heads, int dim, int group);
 hipError_t launch_attn_i4(const AttnI4& a, const AttnPlan& p, bool f16, hipStream_t stream);

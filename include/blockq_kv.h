@@ -60,8 +60,9 @@ bq_status bq_kv_write_i4_f16(const uint16_t* k, int64_t ldk, int64_t hsk, const 
                              int64_t ldv, int64_t hsv, const int32_t* slot, int64_t tokens,
                              const bq_kv_i4* cache, void* stream);
 
-/* The cache -> rows: bf16_rne(fl32(code * scale + least)), one rounding to binary32.  Rows of
- * slots outside the cache become 0; a slot may be named any number of times.  k and v as above,
+/* The cache -> rows: bf16_rne(fl32(code * scale + least)), one rounding to binary32.  A scale that
+ * was rounded up can take a group's largest number past the type's range; it comes back infinite then.
+ * Rows of slots outside the cache become 0; a slot may be named any number of times.  k and v as above,
  * apart from each other, heads and tokens that do not overlap. */
 bq_status bq_kv_read_i4(const bq_kv_i4* cache, const int32_t* slot, int64_t tokens, uint16_t* k,
                         int64_t ldk, int64_t hsk, uint16_t* v, int64_t ldv, int64_t hsv,
@@ -84,14 +85,14 @@ bq_status bq_kv_read_i4_f16(const bq_kv_i4* cache, const int32_t* slot, int64_t 
  * codes and scales hold (but for the bits that much larger scales of v cost, see below).
  *
  * Scores, softmax and sums are in binary32; q is exact but for numbers 2^-24 below the largest of
- * their row.  Before the product with the values, exp(score_t - lse) is held to half a step of
- * binary16 (2^-11 relative; in the _f16 calls 2^-21), and so is v_t where a call has many rows.
- * In the _f16 calls v_t may be beyond binary16's range; it is read back as an infinity, but counts as what
- * it is here.  Values of v that are 2^-16 of the largest of their sequence and head or less lose further
- * bits, the smaller the more; weights and lse do not go by the values, whose scales and least values are at
- * most 2^100.  A NaN or an infinity in a row of q makes every value
- * of that row and head NaN, one in the scales of a token does not reach rows that do not see it.
- * The same call gives the same bits.
+ * their row, and in rows below 2^-100.  Before the product with the values, exp(score_t - lse) is
+ * held to half a step of binary16 (2^-11 relative; in the _f16 calls 2^-21), and so is v_t where a
+ * call has many rows.  In the _f16 calls v_t may be beyond binary16's range; it is read back as an
+ * infinity, but counts as what it is here.  Values of v that are 2^-16 of the largest of their
+ * sequence and head or less lose further bits, the smaller the more; weights and lse do not go by
+ * the values.  Scales and least values, of keys too, are at most 2^100.  A NaN or an infinity in a
+ * row of q makes every value of that row and head NaN, one in the scales of a token does not reach
+ * rows that do not see it.  The same call gives the same bits.
  *
  * q, out: row stride ldq, ldo, head stride hsq, hso entries, multiples of 8, 16-byte aligned;
  * rows and heads of out must not overlap.  table: int32, `table_cols` <= ldt entries a sequence;
