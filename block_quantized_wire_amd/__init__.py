@@ -790,6 +790,9 @@ def bq_moe_mm_i4_f16(x, off, c, scale, y, zero=None, group: int = 128, src=None,
 # last dimension contiguous, tokens and heads with any strides that the header allows.  Another
 # type is a TypeError, another shape, layout or device a ValueError.
 
+_MOST = (1 << 30) - 1       # tokens of a sequence
+
+
 class _KvI4(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("ks", _P), ("vs", _P), ("page_stride", _I64),
                 ("head_stride", _I64), ("spage_stride", _I64), ("shead_stride", _I64),
@@ -950,7 +953,7 @@ def _attn_i4(name, dtype, q, cache, table, lens, out, starts, max_q, max_len, ca
     stream = _on_current(name, cache, stream)
     status = fn(q.data_ptr(), qs[0], qs[1], cache.address, table.data_ptr(), ldt if seqs > 1 else cols,
                 cols, lens.data_ptr(), starts_at, seqs, rows, max_q,
-                cols * cache.page_size if max_len is None else max_len, heads, causal, window, scale,
+                min(cols * cache.page_size, _MOST) if max_len is None else max_len, heads, causal, window, scale,
                 out.data_ptr(), os_[0], os_[1], lse_at, ws_at, ws_bytes, stream)
     if status:
         _check(name, status)
